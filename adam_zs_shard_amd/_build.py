@@ -28,7 +28,8 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
 # Device code is split over several translation units (the fused kernels per
 # gradient dtype) so that they compile in parallel.
 SOURCES = ["zs_fused_f16.hip", "zs_fused_bf16.hip", "zs_table.hip", "zs_unfused.hip",
-           "zs_common.hip", "zs_capi.cpp", "zs_offload.cpp"]
+           "zs_common.hip", "zs_adamw32.hip", "zs_adamw8.hip", "zs_adamw_norm.hip",
+           "zs_capi.cpp", "zs_offload.cpp", "zs_adamw.cpp"]
 # Host-only code (the CPU offload update), compiled as plain C++: SIMD code
 # paths are selected per function with target attributes.
 HOST_SOURCES = ["zs_cpu.cpp"]

@@ -1,0 +1,345 @@
+// zs_adamw.cpp -- host side of the AdamW operators: argument checks, the
+// launch table, the step's constants.  Every argument error is returned before
+// anything touches the device.
+
+#include <hip/hip_runtime_api.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <vector>
+
+#include "zs_adamw.h"
+
+namespace {
+
+constexpr int64_t kMaxLen = int64_t{1} << 60;
+// A launch counts its lanes in 32 bits: 2^24 workgroups of 256 at most.
+constexpr int64_t kMaxChunks = (int64_t{1} << 24) - 1;
+
+// Elements per workgroup.
+constexpr int64_t kChunkLarge = 8192, kChunkSmall = 2048;
+
+int64_t chunk_rule(int64_t total) {
+  return total >= 512 * kChunkLarge ? kChunkLarge : kChunkSmall;
+}
+
+struct Layout {
+  size_t chunks, gptrs, partial, total;
+};
+
+size_t up256(size_t x) { return (x + 255u) & ~static_cast<size_t>(255u); }
+
+// Workgroups' entries, rank pointers, partial sums; false if too large.
+template <class Len>
+bool plan(int32_t npieces, int32_t p, Len len, int64_t* chunk, int64_t* nchunks, Layout* out) {
+  int64_t total = 0;
+  for (int32_t i = 0; i < npieces; ++i) {
+    if (len(i) < 1 || len(i) > kMaxLen || total > kMaxLen - len(i)) return false;
+    total += len(i);
+  }
+  *chunk = chunk_rule(total);
+  *nchunks = 0;
+  for (int32_t i = 0; i < npieces; ++i) *nchunks += (len(i) - 1) / *chunk + 1;
+  if (*nchunks > kMaxChunks) return false;
+  out->chunks = 0;
+  out->gptrs = up256(sizeof(zs::AwChunk) * static_cast<size_t>(*nchunks));
+  out->partial =
+      out->gptrs + up256(sizeof(void*) * static_cast<size_t>(npieces) * static_cast<size_t>(p));
+  out->total = out->partial + up256(sizeof(double) * zs::kSumsqBlocks);
+  return true;
+}
+
+struct Span {
+  uintptr_t lo, hi;
+};
+
+bool grad_dtype_ok(int32_t dt) { return dt == ZS_F16 || dt == ZS_BF16 || dt == ZS_F32; }
+bool param_dtype_ok(int32_t dt) { return dt == 0 || dt == ZS_F16 || dt == ZS_BF16; }
+
+zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32_t grad_dtype,
+                 int32_t param_dtype, int32_t state_bits, void* workspace, size_t ws_bytes,
+                 void* stream, zs_adamw_table* table) {
+  if (!table || !workspace || (npieces > 0 && !pieces)) return ZS_ERR_NULL;
+  if (p < 1 || p > ZS_MAX_P || npieces < 0 ||
+      (state_bits != 0 && state_bits != 8 && state_bits != 32))
+    return ZS_ERR_ARG;
+  if (!grad_dtype_ok(grad_dtype) || !param_dtype_ok(param_dtype)) return ZS_ERR_DTYPE;
+  const uintptr_t gsize = grad_dtype == ZS_F32 ? 4 : 2, ssize = state_bits == 8 ? 1 : 4;
+
+  std::vector<Span> writes, reads;
+  bool aligned = true;
+  const auto span = [&](std::vector<Span>& to, const void* at, uintptr_t size, int64_t n) {
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(at);
+    aligned = aligned && lo % size == 0;
+    to.push_back({lo, lo + size * static_cast<uintptr_t>(n)});
+  };
+  bool all_mean = npieces > 0;
+  for (int32_t i = 0; i < npieces; ++i) {
+    const zs_adamw_piece& q = pieces[i];
+    if (q.len < 1 || q.len > kMaxLen || q.index < 0 || q.index > kMaxLen) return ZS_ERR_ARG;
+    if (!q.grads) return ZS_ERR_NULL;
+    for (int32_t r = 0; r < p; ++r) {
+      if (!q.grads[r]) return ZS_ERR_NULL;
+      span(reads, q.grads[r], gsize, q.len);
+    }
+    all_mean = all_mean && q.g_mean;
+    if (q.g_mean) span(writes, q.g_mean, 4, q.len);
+    if (state_bits == 0) continue;
+    if (!std::isfinite(q.weight_decay) || q.weight_decay < 0.0 || !std::isfinite(q.lr_scale))
+      return ZS_ERR_ARG;
+    if (!q.w || !q.m || !q.v || (param_dtype != 0 && !q.param)) return ZS_ERR_NULL;
+    span(writes, q.w, 4, q.len);
+    span(writes, q.m, ssize, q.len);
+    span(writes, q.v, ssize, q.len);
+    if (param_dtype != 0) span(writes, q.param, 2, q.len);
+    if (state_bits == 8) {
+      if (!q.m_scale || !q.v_scale) return ZS_ERR_NULL;
+      const int64_t nb = (q.len - 1) / ZS_STATE8_BLOCK + 1;
+      span(writes, q.m_scale, 4, nb);
+      span(writes, q.v_scale, 4, nb);
+    }
+  }
+  if (!aligned) return ZS_ERR_ARG;
+
+  Layout lay;
+  int64_t chunk, nchunks;
+  if (!plan(npieces, p, [&](int32_t i) { return pieces[i].len; }, &chunk, &nchunks, &lay))
+    return ZS_ERR_RANGE;
+  if (reinterpret_cast<uintptr_t>(workspace) % 256u != 0 || ws_bytes < lay.total)
+    return ZS_ERR_CAPACITY;
+
+  // Nothing written may meet anything else: sort, then sweep.
+  const uintptr_t ws = reinterpret_cast<uintptr_t>(workspace);
+  writes.push_back({ws, ws + lay.total});
+  const auto by_lo = [](const Span& x, const Span& y) { return x.lo < y.lo; };
+  std::sort(writes.begin(), writes.end(), by_lo);
+  std::sort(reads.begin(), reads.end(), by_lo);
+  for (size_t i = 1; i < writes.size(); ++i)
+    if (writes[i].lo < writes[i - 1].hi) return ZS_ERR_ALIAS;
+  size_t j = 0;
+  uintptr_t reach = 0;  // the furthest end of a read that begins before this write's end
+  for (const Span& wr : writes) {
+    for (; j < reads.size() && reads[j].lo < wr.hi; ++j) reach = std::max(reach, reads[j].hi);
+    if (reach > wr.lo) return ZS_ERR_ALIAS;
+  }
+
+  std::vector<unsigned char> host(lay.partial, 0);
+  auto* chunks = reinterpret_cast<zs::AwChunk*>(host.data() + lay.chunks);
+  auto* gptrs = reinterpret_cast<const void**>(host.data() + lay.gptrs);
+  int64_t c = 0;
+  for (int32_t i = 0; i < npieces; ++i) {
+    const zs_adamw_piece& q = pieces[i];
+    for (int32_t r = 0; r < p; ++r) gptrs[static_cast<int64_t>(i) * p + r] = q.grads[r];
+    for (int64_t at = 0; at < q.len; at += chunk) {
+      zs::AwChunk& d = chunks[c++];
+      if (state_bits != 0) {
+        d.w = q.w + at;
+        d.m = static_cast<char*>(q.m) + at * static_cast<int64_t>(ssize);
+        d.v = static_cast<char*>(q.v) + at * static_cast<int64_t>(ssize);
+        if (state_bits == 8) {
+          d.m_scale = q.m_scale + at / ZS_STATE8_BLOCK;
+          d.v_scale = q.v_scale + at / ZS_STATE8_BLOCK;
+        }
+        if (param_dtype != 0) d.param = static_cast<uint16_t*>(q.param) + at;
+        d.lr_scale = q.lr_scale;
+        d.decay = q.weight_decay;
+      }
+      d.g = static_cast<const char*>(q.grads[0]) + at * static_cast<int64_t>(gsize);
+      if (q.g_mean) d.g_mean = q.g_mean + at;
+      d.index = q.index + at;
+      d.start = at;
+      d.len = static_cast<int32_t>(std::min(chunk, q.len - at));
+      d.piece = i;
+    }
+  }
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!host.empty()) {
+    hipError_t e = hipMemcpyAsync(workspace, host.data(), host.size(), hipMemcpyHostToDevice, s);
+    if (e != hipSuccess) return static_cast<zs_status>(zs::hip_status(e));
+    e = hipStreamSynchronize(s);
+    if (e != hipSuccess) return static_cast<zs_status>(zs::hip_status(e));
+  }
+  table->workspace = workspace;
+  table->nchunks = nchunks;
+  table->chunk_elems = chunk;
+  table->npieces = npieces;
+  table->p = p;
+  table->grad_dtype = grad_dtype;
+  table->param_dtype = state_bits != 0 ? param_dtype : 0;
+  table->state_bits = state_bits;
+  table->has_mean = all_mean ? 1 : 0;
+  return ZS_OK;
+}
+
+zs_status check_table(const zs_adamw_table* t) {
+  if (!t || !t->workspace) return ZS_ERR_NULL;
+  if (t->p < 1 || t->p > ZS_MAX_P || t->npieces < 0 || t->nchunks < t->npieces ||
+      t->nchunks > kMaxChunks || (t->chunk_elems != kChunkLarge && t->chunk_elems != kChunkSmall) ||
+      (t->state_bits != 0 && t->state_bits != 8 && t->state_bits != 32))
+    return ZS_ERR_ARG;
+  if (!grad_dtype_ok(t->grad_dtype) || !param_dtype_ok(t->param_dtype)) return ZS_ERR_DTYPE;
+  return ZS_OK;
+}
+
+zs_status check_hparams(const zs_adamw_hparams* h) {
+  if (!h) return ZS_ERR_NULL;
+  if (!std::isfinite(h->lr) || !std::isfinite(h->eps) || h->eps < 0.0) return ZS_ERR_ARG;
+  if (!(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0))
+    return ZS_ERR_ARG;
+  if (h->step < 1 || !std::isfinite(h->grad_scale) || h->grad_scale == 0.0) return ZS_ERR_ARG;
+  if (!std::isfinite(h->max_norm) || h->max_norm < 0.0) return ZS_ERR_ARG;
+  if (h->rounding != ZS_ROUND_NEAREST && h->rounding != ZS_ROUND_STOCHASTIC) return ZS_ERR_ARG;
+  if (h->skip_nonfinite != 0 && h->skip_nonfinite != 1) return ZS_ERR_ARG;
+  return ZS_OK;
+}
+
+zs::AwConsts make_consts(const zs_adamw_hparams& h, int32_t p, int32_t bits) {
+  zs::AwConsts c;
+  const double t = static_cast<double>(h.step);
+  const double bc1 = 1.0 - std::pow(h.beta1, t), bc2 = 1.0 - std::pow(h.beta2, t);
+  c.B1 = static_cast<float>(h.beta1);
+  c.C1 = static_cast<float>(1.0 - h.beta1);
+  c.B2 = static_cast<float>(h.beta2);
+  c.C2 = static_cast<float>(1.0 - h.beta2);
+  c.A1 = static_cast<float>(bits == 32 ? bc1 : 1.0 / bc1);
+  c.A2 = static_cast<float>(bits == 32 ? bc2 : 1.0 / std::sqrt(bc2));
+  c.EPS = static_cast<float>(h.eps);
+  c.PF = static_cast<float>(static_cast<double>(p));
+  c.lr = h.lr;
+  c.step = h.step;
+  return c;
+}
+
+// Where the workspace's parts lie: the table's own sizes decide.
+Layout layout_of(const zs_adamw_table& t) {
+  Layout l;
+  l.chunks = 0;
+  l.gptrs = up256(sizeof(zs::AwChunk) * static_cast<size_t>(t.nchunks));
+  l.partial = l.gptrs + up256(sizeof(void*) * static_cast<size_t>(t.npieces) *
+                              static_cast<size_t>(t.p));
+  l.total = l.partial + up256(sizeof(double) * zs::kSumsqBlocks);
+  return l;
+}
+
+zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_hparams* hp, const double* sumsq,
+                     void* stream) {
+  if (const zs_status st = check_table(t)) return st;
+  if (const zs_status st = check_hparams(hp)) return st;
+  if (t->state_bits == 0) return ZS_ERR_ARG;
+  if (!sumsq && (hp->max_norm > 0.0 || hp->skip_nonfinite)) return ZS_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(sumsq) % sizeof(double) != 0) return ZS_ERR_ARG;
+  if (t->nchunks == 0) return ZS_OK;
+  const Layout lay = layout_of(*t);
+  auto* base = static_cast<unsigned char*>(t->workspace);
+  zs::AwLaunch L;
+  L.a.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
+  L.a.gptrs = reinterpret_cast<const void* const*>(base + lay.gptrs);
+  L.a.sumsq = sumsq;
+  L.a.grad_scale = hp->grad_scale;
+  L.a.max_norm = hp->max_norm;
+  L.a.seed = hp->seed;
+  L.a.p = t->p;
+  L.a.skip_nonfinite = hp->skip_nonfinite;
+  L.a.c = make_consts(*hp, t->p, t->state_bits);
+  L.nchunks = t->nchunks;
+  L.gdt = t->grad_dtype;
+  L.pdt = t->param_dtype ? t->param_dtype : ZS_BF16;
+  L.bits = t->state_bits;
+  L.rounding = hp->rounding;
+  L.stream = static_cast<hipStream_t>(stream);
+  const hipError_t e = t->state_bits == 32 ? zs::launch_adamw32(L) : zs::launch_adamw8(L);
+  return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
+}
+
+zs_status convert_args(const float* x, const void* codes, const float* scales, int64_t n,
+                       int32_t kind) {
+  if (kind != ZS_STATE8_M && kind != ZS_STATE8_V) return ZS_ERR_ARG;
+  if (n < 0) return ZS_ERR_ARG;
+  if (n > kMaxLen) return ZS_ERR_RANGE;
+  if (n == 0) return ZS_OK;
+  if (!x || !codes || !scales) return ZS_ERR_NULL;
+  const uintptr_t px = reinterpret_cast<uintptr_t>(x), pc = reinterpret_cast<uintptr_t>(codes),
+                  ps = reinterpret_cast<uintptr_t>(scales), u = static_cast<uintptr_t>(n);
+  if (px % 4 != 0 || ps % 4 != 0) return ZS_ERR_ARG;
+  const Span s[3] = {{px, px + 4 * u},
+                     {pc, pc + u},
+                     {ps, ps + 4 * ((u - 1) / ZS_STATE8_BLOCK + 1)}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (s[i].lo < s[j].hi && s[j].lo < s[i].hi) return ZS_ERR_ALIAS;
+  return ZS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t zs_adamw_workspace_bytes(const int64_t* lens, int32_t npieces, int32_t p) {
+  if (npieces < 0 || (npieces > 0 && !lens) || p < 1 || p > ZS_MAX_P) return 0;
+  Layout lay;
+  int64_t chunk, nchunks;
+  if (!plan(npieces, p, [&](int32_t i) { return lens[i]; }, &chunk, &nchunks, &lay)) return 0;
+  return lay.total;
+}
+
+zs_status zs_adamw_upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p,
+                          int32_t grad_dtype, int32_t param_dtype, int32_t state_bits,
+                          void* workspace, size_t ws_bytes, void* stream, zs_adamw_table* table) {
+  return zs::guard([&] {
+    return upload(pieces, npieces, p, grad_dtype, param_dtype, state_bits, workspace, ws_bytes,
+                  stream, table);
+  });
+}
+
+zs_status zs_adamw_step_multi(const zs_adamw_table* table, const zs_adamw_hparams* hp,
+                              const double* sumsq, void* stream) {
+  return zs::guard([&] { return adamw_step(table, hp, sumsq, stream); });
+}
+
+zs_status zs_grad_sumsq_multi(const zs_adamw_table* t, int32_t store_mean, int32_t accumulate,
+                              double* sumsq, void* stream) {
+  return zs::guard([&]() -> zs_status {
+    if (const zs_status st = check_table(t)) return st;
+    if (!sumsq) return ZS_ERR_NULL;
+    if ((store_mean != 0 && store_mean != 1) || (accumulate != 0 && accumulate != 1) ||
+        reinterpret_cast<uintptr_t>(sumsq) % sizeof(double) != 0)
+      return ZS_ERR_ARG;
+    if (store_mean && t->npieces > 0 && !t->has_mean) return ZS_ERR_NULL;
+    const Layout lay = layout_of(*t);
+    auto* base = static_cast<unsigned char*>(t->workspace);
+    zs::SumsqLaunch L;
+    L.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
+    L.gptrs = reinterpret_cast<const void* const*>(base + lay.gptrs);
+    L.nchunks = t->nchunks;
+    L.p = t->p;
+    L.gdt = t->grad_dtype;
+    L.store = store_mean != 0;
+    L.accumulate = accumulate != 0;
+    L.partial = reinterpret_cast<double*>(base + lay.partial);
+    L.out = sumsq;
+    L.stream = static_cast<hipStream_t>(stream);
+    const hipError_t e = zs::launch_sumsq(L);
+    return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
+  });
+}
+
+zs_status zs_state8_encode(const float* x, int64_t n, int32_t kind, void* codes, float* scales,
+                           void* stream) {
+  if (const zs_status st = convert_args(x, codes, scales, n, kind)) return st;
+  if (n == 0) return ZS_OK;
+  const hipError_t e = zs::launch_state8_encode(x, n, kind, codes, scales,
+                                                static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
+}
+
+zs_status zs_state8_decode(const void* codes, const float* scales, int64_t n, int32_t kind,
+                           float* x, void* stream) {
+  if (const zs_status st = convert_args(x, codes, scales, n, kind)) return st;
+  if (n == 0) return ZS_OK;
+  const hipError_t e = zs::launch_state8_decode(codes, scales, n, kind, x,
+                                                static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
+}
+
+}  // extern "C"

@@ -1,0 +1,80 @@
+// zs_adamw.h -- the AdamW operators' launch descriptions (host and device).
+#pragma once
+
+#include "../../include/zsadamw.h"
+#include "zs_internal.h"
+
+namespace zs {
+
+constexpr int kF32 = ZS_F32;
+constexpr int kStateBlock = ZS_STATE8_BLOCK;  // one wave: 64 lanes x 4 elements
+
+// One workgroup's share of one tensor, with every address at its first
+// element, so that a wave knows all it needs after one scalar load.
+struct AwChunk {
+  float* w;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  uint16_t* param;
+  const void* g;      // rank 0's gradient
+  float* g_mean;
+  int64_t index;      // of element 0, for the random bits
+  int64_t start;      // of element 0 in its tensor
+  double lr_scale;
+  double decay;
+  int32_t len;
+  int32_t piece;
+  int64_t reserved[3];
+};
+static_assert(sizeof(AwChunk) == 128, "one table entry per 128-byte line");
+
+// The scalars of one step, each computed in double and rounded once.
+struct AwConsts {
+  float B1, C1, B2, C2;
+  float A1, A2;  // 32-bit states: 1-beta1^t, 1-beta2^t; 8-bit: f32(1/(1-beta1^t)), f32(1/sqrt(1-beta2^t))
+  float EPS, PF;
+  double lr;
+  int64_t step;
+};
+
+struct AwArgs {
+  const AwChunk* chunks;
+  const void* const* gptrs;  // npieces * p rank pointers at the tensors' first elements
+  const double* sumsq;       // or null
+  double grad_scale, max_norm;
+  uint64_t seed;
+  int32_t p;
+  int32_t skip_nonfinite;
+  AwConsts c;
+};
+
+struct AwLaunch {
+  AwArgs a;
+  int64_t nchunks;
+  int gdt, pdt, bits, rounding;
+  hipStream_t stream;
+};
+
+struct SumsqLaunch {
+  const AwChunk* chunks;
+  const void* const* gptrs;
+  int64_t nchunks;
+  int p, gdt;
+  bool store, accumulate;
+  double* partial;  // kSumsqBlocks doubles
+  double* out;
+  hipStream_t stream;
+};
+constexpr int kSumsqBlocks = 2048;  // workgroups of a sum of squares at most
+
+hipError_t launch_adamw32(const AwLaunch& a);
+hipError_t launch_adamw8(const AwLaunch& a);
+hipError_t launch_sumsq(const SumsqLaunch& a);
+hipError_t launch_state8_encode(const float* x, int64_t n, int kind, void* codes, float* scales,
+                                hipStream_t stream);
+hipError_t launch_state8_decode(const void* codes, const float* scales, int64_t n, int kind,
+                                float* x, hipStream_t stream);
+
+}  // namespace zs

@@ -1,0 +1,338 @@
+// zs_adamw_device.h -- device code shared by the AdamW kernels of libzshard.
+//
+// The AdamW step streams: per element p gradients, the fp32 master weight and
+// the two moments in, the weight, the moments and the 16-bit copy out, and
+// about 50 fp32 operations, so HBM bounds it (28 bytes per element with one
+// bf16 gradient and 32-bit moments, 16.06 with 8-bit ones).  The unit is a
+// block of 256 elements and one wave: lane l holds elements 4l .. 4l+3, so
+// each access is one whole-line stream (fp32 1 KiB, 16-bit 512 bytes, codes
+// 256 bytes per instruction), the largest value of an 8-bit block is one
+// reduction over the wave, and no wave waits for another.
+#pragma once
+
+#include "zs_adamw.h"
+#include "zs_device.h"
+
+#pragma clang fp contract(off)
+
+namespace zs {
+namespace {
+
+constexpr int kQuad = 4;
+constexpr int kWave = 64;
+constexpr int kWaves = kBlock / kWave;
+
+// Codes may sit at any byte address.
+typedef uint32_t u32b __attribute__((aligned(1)));
+
+template <class F>
+void with_gdt(int dt, F&& f) {
+  if (dt == kF16) f(IC<kF16>{});
+  else if (dt == kBF16) f(IC<kBF16>{});
+  else f(IC<kF32>{});
+}
+
+// ---- four elements of a lane ------------------------------------------------
+template <int DT>
+struct Raw4 {
+  u32x2 x;
+};
+template <>
+struct Raw4<kF32> {
+  f32x4 x;
+};
+
+template <int DT>
+constexpr int kSize = DT == kF32 ? 4 : 2;
+
+template <int DT>
+__device__ __forceinline__ Raw4<DT> ld_raw4(const void* base, uint32_t lane) {
+  const char* p = static_cast<const char*>(base) + lane * (kQuad * kSize<DT>);
+  if constexpr (DT == kF32)
+    return Raw4<DT>{__builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p))};
+  else
+    return Raw4<DT>{__builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p))};
+}
+// The first n (0..4) of the lane's elements, zeros behind them.
+template <int DT>
+__device__ __forceinline__ Raw4<DT> ld_raw4(const void* base, uint32_t lane, int n) {
+  if constexpr (DT == kF32) {
+    const float* p = static_cast<const float*>(base) + lane * kQuad;
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j)
+      if (j < n) x[j] = p[j];
+    return Raw4<DT>{x};
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + lane * kQuad;
+    uint32_t h[kQuad] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j)
+      if (j < n) h[j] = p[j];
+    return Raw4<DT>{u32x2{h[0] | h[1] << 16, h[2] | h[3] << 16}};
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void widen4(const Raw4<DT>& q, float (&x)[kQuad]) {
+  if constexpr (DT == kF32) {
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j) x[j] = q.x[j];
+  } else {
+    x[0] = widen_lo<DT>(q.x[0]);
+    x[1] = widen_hi<DT>(q.x[0]);
+    x[2] = widen_lo<DT>(q.x[1]);
+    x[3] = widen_hi<DT>(q.x[1]);
+  }
+}
+
+__device__ __forceinline__ void st_quad32(float* base, uint32_t lane, const float (&x)[kQuad]) {
+  __builtin_nontemporal_store(f32x4{x[0], x[1], x[2], x[3]},
+                              reinterpret_cast<f32x4*>(base + lane * kQuad));
+}
+__device__ __forceinline__ void st_quad32(float* base, uint32_t lane, int n,
+                                          const float (&x)[kQuad]) {
+#pragma unroll
+  for (int j = 0; j < kQuad; ++j)
+    if (j < n) base[lane * kQuad + j] = x[j];
+}
+template <int DT>
+__device__ __forceinline__ void st_quad16(uint16_t* base, uint32_t lane, const float (&x)[kQuad]) {
+  __builtin_nontemporal_store(u32x2{narrow2<DT>(x[0], x[1]), narrow2<DT>(x[2], x[3])},
+                              reinterpret_cast<u32x2*>(base + lane * kQuad));
+}
+template <int DT>
+__device__ __forceinline__ void st_quad16(uint16_t* base, uint32_t lane, int n,
+                                          const float (&x)[kQuad]) {
+#pragma unroll
+  for (int j = 0; j < kQuad; ++j)
+    if (j < n) base[lane * kQuad + j] = narrow1<DT>(x[j]);
+}
+// Four codes, one per byte.
+__device__ __forceinline__ uint32_t ld_codes(const void* base, uint32_t lane) {
+  return __builtin_nontemporal_load(
+      reinterpret_cast<const u32b*>(static_cast<const char*>(base) + lane * kQuad));
+}
+__device__ __forceinline__ uint32_t ld_codes(const void* base, uint32_t lane, int n) {
+  const uint8_t* p = static_cast<const uint8_t*>(base) + lane * kQuad;
+  uint32_t x = 0;
+#pragma unroll
+  for (int j = 0; j < kQuad; ++j)
+    if (j < n) x |= static_cast<uint32_t>(p[j]) << (8 * j);
+  return x;
+}
+__device__ __forceinline__ void st_codes(void* base, uint32_t lane, uint32_t x) {
+  __builtin_nontemporal_store(
+      x, reinterpret_cast<u32b*>(static_cast<char*>(base) + lane * kQuad));
+}
+__device__ __forceinline__ void st_codes(void* base, uint32_t lane, int n, uint32_t x) {
+  uint8_t* p = static_cast<uint8_t*>(base) + lane * kQuad;
+#pragma unroll
+  for (int j = 0; j < kQuad; ++j)
+    if (j < n) p[j] = static_cast<uint8_t>(x >> (8 * j));
+}
+
+// ---- gradients ----------------------------------------------------------------
+typedef const void* const __attribute__((address_space(4)))* RankPtrs;
+
+// Loads of R ranks for U blocks in flight together, then the adds in rank
+// order.  n < 0: whole blocks.
+template <int R, int U, int GDT>
+__device__ __forceinline__ void add_ranks(RankPtrs ptrs, int r0, int64_t byte0, uint32_t lane,
+                                          int n, float (&s)[U][kQuad]) {
+  Raw4<GDT> q[R][U];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const char* base = static_cast<const char*>(ptrs[r0 + r]) + byte0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const char* b = base + u * (kStateBlock * kSize<GDT>);
+      q[r][u] = n < 0 ? ld_raw4<GDT>(b, lane) : ld_raw4<GDT>(b, lane, n);
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[kQuad];
+      widen4<GDT>(q[r][u], x);
+#pragma unroll
+      for (int j = 0; j < kQuad; ++j) s[u][j] = r0 + r == 0 ? x[j] : s[u][j] + x[j];
+    }
+}
+
+// The rank-order mean of U blocks that start `at` elements into their tensor.
+template <int U, int GDT>
+__device__ __forceinline__ void mean_ranks(RankPtrs ptrs, int p, float PF, int64_t at,
+                                           uint32_t lane, int n, float (&s)[U][kQuad]) {
+  const int64_t byte0 = at * kSize<GDT>;
+  int r = 0;
+  for (; r + 4 <= p; r += 4) add_ranks<4, U, GDT>(ptrs, r, byte0, lane, n, s);
+  if (r + 2 <= p) {
+    add_ranks<2, U, GDT>(ptrs, r, byte0, lane, n, s);
+    r += 2;
+  }
+  if (r < p) add_ranks<1, U, GDT>(ptrs, r, byte0, lane, n, s);
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j) s[u][j] = s[u][j] / PF;
+}
+
+// ---- 8-bit moments ------------------------------------------------------------
+constexpr float kTopM = 448.0f, kTopV = 57344.0f;
+constexpr uint32_t kTinyBits = (127u - 110u) << 23;  // 2^-110
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
+  const uint32_t y = static_cast<uint32_t>(
+      __builtin_amdgcn_update_dpp(0, static_cast<int>(x), CTRL, 0xf, 0xf, true));
+  return x > y ? x : y;
+}
+
+// The largest of the wave's values (fp32 magnitudes compare as their bits,
+// NaN above infinity above the rest).  Every lane must be active.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = dpp_max<0xb1>(x);   // lanes xor 1
+  x = dpp_max<0x4e>(x);   // xor 2
+  x = dpp_max<0x141>(x);  // mirrored in eights
+  x = dpp_max<0x140>(x);  // mirrored in sixteens
+  const uint32_t a = __builtin_amdgcn_readlane(x, 0), b = __builtin_amdgcn_readlane(x, 16);
+  const uint32_t c = __builtin_amdgcn_readlane(x, 32), d = __builtin_amdgcn_readlane(x, 48);
+  const uint32_t ab = a > b ? a : b, cd = c > d ? c : d;
+  return ab > cd ? ab : cd;
+}
+
+__device__ __forceinline__ uint32_t mag_bits(float x) {
+  return __float_as_uint(x) & 0x7fffffffu;
+}
+
+struct BlockScale {
+  float scale;    // stored
+  float inverse;  // the values' factor before they are rounded
+};
+
+template <int KIND>
+__device__ __forceinline__ BlockScale block_scale(uint32_t most) {
+  constexpr float top = KIND == ZS_STATE8_M ? kTopM : kTopV;
+  constexpr float down = static_cast<float>(1.0 / static_cast<double>(top));
+  BlockScale s{0.0f, 0.0f};
+  if (most >= kTinyBits) {
+    s.scale = __uint_as_float(most) * down;
+    s.inverse = top / __uint_as_float(most);
+  }
+  if (most >= kInfBits) s.scale = __uint_as_float(0x7fc00000u);
+  return s;
+}
+
+// Random rounding: y's magnitude on the grid of its type, up with the
+// probability that its place between two neighbours says (16 bits of it).
+template <int KIND>
+__device__ __forceinline__ float to_grid(float y, uint32_t half) {
+  constexpr int kCut = KIND == ZS_STATE8_M ? 20 : 21;
+  constexpr float kLeast = KIND == ZS_STATE8_M ? 0x1p-6f : 0x1p-14f;
+  const float mag = __builtin_fabsf(y);
+  const bool low = mag < kLeast;  // the even part of the grid
+  const float up = low ? mag + kLeast : mag;
+  const uint32_t r = (half << (kCut - 16)) + (1u << (kCut - 17));
+  const float cut = __uint_as_float((__float_as_uint(up) + r) & ~((1u << kCut) - 1u));
+  return __builtin_copysignf(low ? cut - kLeast : cut, y);
+}
+
+// Four values to codes: x * inverse cut to [-top, top], to the nearest code
+// (or to_grid's), a positive v never to code 0.
+template <int KIND, bool RANDOM>
+__device__ __forceinline__ uint32_t encode4(const float (&x)[kQuad], const BlockScale& s,
+                                            const uint32_t (&half)[kQuad]) {
+  constexpr float top = KIND == ZS_STATE8_M ? kTopM : kTopV;
+  float y[kQuad];
+#pragma unroll
+  for (int j = 0; j < kQuad; ++j) {
+    y[j] = __builtin_fminf(__builtin_fmaxf(x[j] * s.inverse, -top), top);
+    if constexpr (RANDOM) y[j] = to_grid<KIND>(y[j], half[j]);
+  }
+  int c = 0;
+  if constexpr (KIND == ZS_STATE8_M) {
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], c, false);
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
+  } else {
+    c = __builtin_amdgcn_cvt_pk_bf8_f32(y[0], y[1], c, false);
+    c = __builtin_amdgcn_cvt_pk_bf8_f32(y[2], y[3], c, true);
+  }
+  uint32_t u = static_cast<uint32_t>(c);
+  if constexpr (KIND == ZS_STATE8_V) {
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j)
+      if (x[j] > 0.0f && ((u >> (8 * j)) & 0xffu) == 0u) u |= 1u << (8 * j);
+  }
+  return s.scale > 0.0f ? u : 0u;  // no codes for a block of zeros or a NaN scale
+}
+
+template <int KIND>
+__device__ __forceinline__ void decode4(uint32_t c, float scale, float (&x)[kQuad]) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  f32x2 a, b;
+  if constexpr (KIND == ZS_STATE8_M) {
+    a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c), false);
+    b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(c), true);
+  } else {
+    a = __builtin_amdgcn_cvt_pk_f32_bf8(static_cast<int>(c), false);
+    b = __builtin_amdgcn_cvt_pk_f32_bf8(static_cast<int>(c), true);
+  }
+  x[0] = a[0] * scale;
+  x[1] = a[1] * scale;
+  x[2] = b[0] * scale;
+  x[3] = b[1] * scale;
+}
+
+// Philox4x32 with 7 rounds (Salmon et al., SC'11): four random words from a
+// counter and a key.
+__device__ __forceinline__ void philox(uint64_t at, uint64_t step, uint64_t seed,
+                                       uint32_t (&w)[kQuad]) {
+  uint32_t c0 = static_cast<uint32_t>(at), c1 = static_cast<uint32_t>(at >> 32);
+  uint32_t c2 = static_cast<uint32_t>(step), c3 = static_cast<uint32_t>(step >> 32);
+  uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+#pragma unroll
+  for (int i = 0; i < 7; ++i) {
+    const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u;
+    const uint64_t b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c1 = static_cast<uint32_t>(b);
+    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c3 = static_cast<uint32_t>(a);
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  w[0] = c0;
+  w[1] = c1;
+  w[2] = c2;
+  w[3] = c3;
+}
+
+// ---- the step's scalars -------------------------------------------------------
+struct Scalars {
+  float GS;   // the gradient's factor
+  bool skip;  // the norm is not finite and such a step is to be left out
+};
+
+__device__ __forceinline__ Scalars scalars(const AwArgs& a) {
+  if (!a.sumsq) return Scalars{static_cast<float>(a.grad_scale), false};
+  const double norm = __builtin_sqrt(*a.sumsq) * __builtin_fabs(a.grad_scale);
+  const bool finite = __builtin_fabs(norm) < __builtin_inf();
+  double coef = 1.0;
+  if (a.max_norm > 0.0) {
+    coef = a.max_norm / (norm + 1e-6);
+    coef = coef > 1.0 ? 1.0 : coef;  // NaN stays
+  }
+  return Scalars{static_cast<float>(a.grad_scale * coef), a.skip_nonfinite != 0 && !finite};
+}
+
+// One element's moments, in the order of the fp32 definition.
+__device__ __forceinline__ void moments1(const AwConsts& c, float g, float& m, float& v) {
+  m = c.B1 * m + c.C1 * g;
+  v = c.B2 * v + c.C2 * (g * g);
+}
+
+}  // namespace
+}  // namespace zs

@@ -1,0 +1,204 @@
+// zs_adamw_norm.hip -- the sum of squares of the gradient mean, and moments to
+// and from their 8-bit form.
+
+#include "zs_adamw_device.h"
+
+#pragma clang fp contract(off)
+
+namespace zs {
+namespace {
+
+// The sum of the workgroup's values, in a fixed order, to thread 0.
+__device__ __forceinline__ double block_sum(double x) {
+  __shared__ double part[kWaves];
+#pragma unroll
+  for (int d = kWave / 2; d > 0; d /= 2) x += __shfl_xor(x, d, kWave);
+  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = x;
+  __syncthreads();
+  double s = part[0];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) s += part[i];
+  __syncthreads();
+  return s;
+}
+
+template <int U, int GDT, bool STORE, bool ONE>
+__device__ __forceinline__ void sumsq_blocks(const AwChunk& ch, const void* const* gptrs, int p,
+                                             float PF, int b, uint32_t lane, int n, double& acc) {
+  const int64_t e0 = static_cast<int64_t>(b) * kStateBlock;
+  float g[U][kQuad];
+  if constexpr (ONE) {
+    Raw4<GDT> q[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const char* gb = static_cast<const char*>(ch.g) + (e0 + u * kStateBlock) * kSize<GDT>;
+      q[u] = n < 0 ? ld_raw4<GDT>(gb, lane) : ld_raw4<GDT>(gb, lane, n);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) widen4<GDT>(q[u], g[u]);
+  } else {
+    mean_ranks<U, GDT>(
+        (RankPtrs)(reinterpret_cast<uintptr_t>(gptrs + static_cast<int64_t>(ch.piece) * p)), p, PF,
+        ch.start + e0, lane, n, g);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if constexpr (STORE) {
+      if (n < 0)
+        st_quad32(ch.g_mean + e0 + u * kStateBlock, lane, g[u]);
+      else
+        st_quad32(ch.g_mean + e0 + u * kStateBlock, lane, n, g[u]);
+    }
+    // a product of two fp32 values is exact in double
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j)
+      acc = __builtin_fma(static_cast<double>(g[u][j]), static_cast<double>(g[u][j]), acc);
+  }
+}
+
+template <int GDT, bool STORE, bool ONE>
+__global__ __launch_bounds__(kBlock) void sumsq_kernel(const AwChunk* chunks,
+                                                       const void* const* gptrs, int64_t nchunks,
+                                                       int p, float PF, double* partial) {
+  constexpr int U = 4;
+  const uint32_t lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  double acc = 0.0;
+  for (int64_t c = blockIdx.x; c < nchunks; c += gridDim.x) {
+    const AwChunk ch = chunks[c];
+    const int full = ch.len / kStateBlock;
+    const int blocks = (ch.len + kStateBlock - 1) / kStateBlock;
+    for (int b = wave * U; b < blocks; b += kWaves * U) {
+      if (b + U <= full) {
+        sumsq_blocks<U, GDT, STORE, ONE>(ch, gptrs, p, PF, b, lane, -1, acc);
+      } else {
+        for (int k = b; k < b + U && k < blocks; ++k) {
+          int n = ch.len - k * kStateBlock - kQuad * static_cast<int>(lane);
+          n = n < 0 ? 0 : n > kQuad ? kQuad : n;
+          sumsq_blocks<1, GDT, STORE, ONE>(ch, gptrs, p, PF, k, lane, n, acc);
+        }
+      }
+    }
+  }
+  const double s = block_sum(acc);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kBlock) void sumsq_join_kernel(const double* partial, int n,
+                                                            int accumulate, double* out) {
+  double acc = 0.0;
+  for (int i = threadIdx.x; i < n; i += kBlock) acc += partial[i];
+  const double s = block_sum(acc);
+  if (threadIdx.x == 0) *out = accumulate ? *out + s : s;
+}
+
+// One wave per block of 256 values.
+template <int KIND>
+__device__ __forceinline__ void encode_block(const float* x, int64_t n, uint8_t* codes,
+                                             float* scales, int64_t b, uint32_t lane) {
+  const int64_t e = b * kStateBlock;
+  const int64_t left = n - e - kQuad * lane;
+  const int k = left < 0 ? 0 : left > kQuad ? kQuad : static_cast<int>(left);
+  float y[kQuad];
+  widen4<kF32>(n - e >= kStateBlock ? ld_raw4<kF32>(x + e, lane) : ld_raw4<kF32>(x + e, lane, k),
+               y);
+  uint32_t most = 0;
+#pragma unroll
+  for (int j = 0; j < kQuad; ++j) most = mag_bits(y[j]) > most ? mag_bits(y[j]) : most;
+  const BlockScale s = block_scale<KIND>(wave_max(most));
+  const uint32_t none[kQuad] = {0u, 0u, 0u, 0u};
+  const uint32_t c = encode4<KIND, false>(y, s, none);
+  if (n - e >= kStateBlock)
+    st_codes(codes + e, lane, c);
+  else
+    st_codes(codes + e, lane, k, c);
+  if (lane == 0) scales[b] = s.scale;
+}
+
+template <int KIND>
+__device__ __forceinline__ void decode_block(const uint8_t* codes, const float* scales, int64_t n,
+                                             float* x, int64_t b, uint32_t lane) {
+  const int64_t e = b * kStateBlock;
+  const int64_t left = n - e - kQuad * lane;
+  const int k = left < 0 ? 0 : left > kQuad ? kQuad : static_cast<int>(left);
+  float y[kQuad];
+  decode4<KIND>(n - e >= kStateBlock ? ld_codes(codes + e, lane) : ld_codes(codes + e, lane, k),
+                scales[b], y);
+  if (n - e >= kStateBlock)
+    st_quad32(x + e, lane, y);
+  else
+    st_quad32(x + e, lane, k, y);
+}
+
+template <int KIND>
+__global__ __launch_bounds__(kBlock) void encode_kernel(const float* x, int64_t n, uint8_t* codes,
+                                                        float* scales) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  for (int64_t b = static_cast<int64_t>(blockIdx.x) * kWaves + wave; b * kStateBlock < n;
+       b += static_cast<int64_t>(gridDim.x) * kWaves)
+    encode_block<KIND>(x, n, codes, scales, b, threadIdx.x % kWave);
+}
+
+template <int KIND>
+__global__ __launch_bounds__(kBlock) void decode_kernel(const uint8_t* codes, const float* scales,
+                                                        int64_t n, float* x) {
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  for (int64_t b = static_cast<int64_t>(blockIdx.x) * kWaves + wave; b * kStateBlock < n;
+       b += static_cast<int64_t>(gridDim.x) * kWaves)
+    decode_block<KIND>(codes, scales, n, x, b, threadIdx.x % kWave);
+}
+
+unsigned convert_grid(int64_t n) {
+  const int64_t blocks = (n + kStateBlock * kWaves - 1) / (kStateBlock * kWaves);
+  const int64_t most = static_cast<int64_t>(cu_count()) * 8;
+  return static_cast<unsigned>(blocks < most ? blocks : most);
+}
+
+}  // namespace
+
+hipError_t launch_sumsq(const SumsqLaunch& L) {
+  int64_t grid = static_cast<int64_t>(cu_count()) * 4;
+  if (grid > kSumsqBlocks) grid = kSumsqBlocks;
+  if (grid > L.nchunks) grid = L.nchunks;
+  const float PF = static_cast<float>(static_cast<double>(L.p));
+  if (grid > 0) with_gdt(L.gdt, [&](auto G) {
+    constexpr int GDT = decltype(G)::value;
+    const dim3 gd(static_cast<unsigned>(grid)), bd(kBlock);
+    const auto go = [&](auto store, auto one) {
+      sumsq_kernel<GDT, decltype(store)::value != 0, decltype(one)::value != 0>
+          <<<gd, bd, 0, L.stream>>>(L.chunks, L.gptrs, L.nchunks, L.p, PF, L.partial);
+    };
+    if (L.store)
+      L.p == 1 ? go(IC<1>{}, IC<1>{}) : go(IC<1>{}, IC<0>{});
+    else
+      L.p == 1 ? go(IC<0>{}, IC<1>{}) : go(IC<0>{}, IC<0>{});
+  });
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  sumsq_join_kernel<<<dim3(1), dim3(kBlock), 0, L.stream>>>(L.partial, static_cast<int>(grid),
+                                                            L.accumulate ? 1 : 0, L.out);
+  return hipGetLastError();
+}
+
+hipError_t launch_state8_encode(const float* x, int64_t n, int kind, void* codes, float* scales,
+                                hipStream_t stream) {
+  const dim3 gd(convert_grid(n)), bd(kBlock);
+  if (kind == ZS_STATE8_M)
+    encode_kernel<ZS_STATE8_M><<<gd, bd, 0, stream>>>(x, n, static_cast<uint8_t*>(codes), scales);
+  else
+    encode_kernel<ZS_STATE8_V><<<gd, bd, 0, stream>>>(x, n, static_cast<uint8_t*>(codes), scales);
+  return hipGetLastError();
+}
+
+hipError_t launch_state8_decode(const void* codes, const float* scales, int64_t n, int kind,
+                                float* x, hipStream_t stream) {
+  const dim3 gd(convert_grid(n)), bd(kBlock);
+  const uint8_t* c = static_cast<const uint8_t*>(codes);
+  if (kind == ZS_STATE8_M)
+    decode_kernel<ZS_STATE8_M><<<gd, bd, 0, stream>>>(c, scales, n, x);
+  else
+    decode_kernel<ZS_STATE8_V><<<gd, bd, 0, stream>>>(c, scales, n, x);
+  return hipGetLastError();
+}
+
+}  // namespace zs

@@ -1,0 +1,171 @@
+// zs_adamw_step.h -- the AdamW step's kernel, compiled once per width of the
+// moments (zs_adamw32.hip, zs_adamw8.hip).
+#pragma once
+
+#include "zs_adamw_device.h"
+
+#pragma clang fp contract(off)
+
+namespace zs {
+namespace {
+
+// U blocks of 256 elements by one wave, from block b of the chunk on.  n < 0:
+// whole blocks; else (U = 1) the lane's n (0..4) elements of a tensor's last
+// block.
+template <int U, int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
+__device__ __forceinline__ void step_blocks(const AwArgs& a, const AwChunk& ch, float GS, float LR,
+                                            float LD, int b, uint32_t lane, int n) {
+  const int64_t e0 = static_cast<int64_t>(b) * kStateBlock;
+  float g[U][kQuad], w[U][kQuad], m[U][kQuad], v[U][kQuad];
+  Raw4<kF32> wq[U], mq[U], vq[U];
+  uint32_t mc[U], vc[U];
+  float ms[U], vs[U];
+  Raw4<GDT> gq[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t e = e0 + u * kStateBlock;
+    if constexpr (ONE) {
+      const char* gb = static_cast<const char*>(ch.g) + e * kSize<GDT>;
+      gq[u] = n < 0 ? ld_raw4<GDT>(gb, lane) : ld_raw4<GDT>(gb, lane, n);
+    }
+    wq[u] = n < 0 ? ld_raw4<kF32>(ch.w + e, lane) : ld_raw4<kF32>(ch.w + e, lane, n);
+    if constexpr (BITS == 32) {
+      const float* mb = static_cast<const float*>(ch.m) + e;
+      const float* vb = static_cast<const float*>(ch.v) + e;
+      mq[u] = n < 0 ? ld_raw4<kF32>(mb, lane) : ld_raw4<kF32>(mb, lane, n);
+      vq[u] = n < 0 ? ld_raw4<kF32>(vb, lane) : ld_raw4<kF32>(vb, lane, n);
+    } else {
+      const uint8_t* mb = static_cast<const uint8_t*>(ch.m) + e;
+      const uint8_t* vb = static_cast<const uint8_t*>(ch.v) + e;
+      mc[u] = n < 0 ? ld_codes(mb, lane) : ld_codes(mb, lane, n);
+      vc[u] = n < 0 ? ld_codes(vb, lane) : ld_codes(vb, lane, n);
+      ms[u] = ch.m_scale[b + u];
+      vs[u] = ch.v_scale[b + u];
+    }
+  }
+  if constexpr (ONE) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) widen4<GDT>(gq[u], g[u]);
+  } else {
+    mean_ranks<U, GDT>((RankPtrs)(reinterpret_cast<uintptr_t>(
+                           a.gptrs + static_cast<int64_t>(ch.piece) * a.p)),
+                       a.p, a.c.PF, ch.start + e0, lane, n, g);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t e = e0 + u * kStateBlock;
+    widen4<kF32>(wq[u], w[u]);
+    if constexpr (BITS == 32) {
+      widen4<kF32>(mq[u], m[u]);
+      widen4<kF32>(vq[u], v[u]);
+    } else {
+      decode4<ZS_STATE8_M>(mc[u], ms[u], m[u]);
+      decode4<ZS_STATE8_V>(vc[u], vs[u], v[u]);
+    }
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j) {
+      moments1(a.c, g[u][j] * GS, m[u][j], v[u][j]);
+      float x;
+      if constexpr (BITS == 32)
+        x = (m[u][j] / a.c.A1) / (__builtin_sqrtf(v[u][j] / a.c.A2) + a.c.EPS);
+      else
+        x = (m[u][j] * a.c.A1) / (__builtin_sqrtf(v[u][j]) * a.c.A2 + a.c.EPS);
+      w[u][j] = w[u][j] - (LR * x + LD * w[u][j]);
+    }
+    if (n < 0) {
+      st_quad32(ch.w + e, lane, w[u]);
+      if (ch.param) st_quad16<PDT>(ch.param + e, lane, w[u]);
+    } else {
+      st_quad32(ch.w + e, lane, n, w[u]);
+      if (ch.param) st_quad16<PDT>(ch.param + e, lane, n, w[u]);
+    }
+    if constexpr (BITS == 32) {
+      float* mb = static_cast<float*>(ch.m) + e;
+      float* vb = static_cast<float*>(ch.v) + e;
+      if (n < 0) {
+        st_quad32(mb, lane, m[u]);
+        st_quad32(vb, lane, v[u]);
+      } else {
+        st_quad32(mb, lane, n, m[u]);
+        st_quad32(vb, lane, n, v[u]);
+      }
+    } else {
+      // elements behind the tensor's end are zeros here: they raise no maximum
+      uint32_t mm = 0, vm = 0;
+#pragma unroll
+      for (int j = 0; j < kQuad; ++j) {
+        mm = mag_bits(m[u][j]) > mm ? mag_bits(m[u][j]) : mm;
+        vm = mag_bits(v[u][j]) > vm ? mag_bits(v[u][j]) : vm;
+      }
+      const BlockScale sm = block_scale<ZS_STATE8_M>(wave_max(mm));
+      const BlockScale sv = block_scale<ZS_STATE8_V>(wave_max(vm));
+      uint32_t r[kQuad] = {0u, 0u, 0u, 0u}, lo[kQuad], hi[kQuad];
+      if constexpr (RANDOM)
+        philox(static_cast<uint64_t>(ch.index + e + kQuad * lane),
+               static_cast<uint64_t>(a.c.step), a.seed, r);
+#pragma unroll
+      for (int j = 0; j < kQuad; ++j) {
+        lo[j] = r[j] & 0xffffu;
+        hi[j] = r[j] >> 16;
+      }
+      const uint32_t cm = encode4<ZS_STATE8_M, RANDOM>(m[u], sm, lo);
+      const uint32_t cv = encode4<ZS_STATE8_V, RANDOM>(v[u], sv, hi);
+      uint8_t* mb = static_cast<uint8_t*>(ch.m) + e;
+      uint8_t* vb = static_cast<uint8_t*>(ch.v) + e;
+      if (n < 0) {
+        st_codes(mb, lane, cm);
+        st_codes(vb, lane, cv);
+      } else {
+        st_codes(mb, lane, n, cm);
+        st_codes(vb, lane, n, cv);
+      }
+      if (lane == 0) {
+        ch.m_scale[b + u] = sm.scale;
+        ch.v_scale[b + u] = sv.scale;
+      }
+    }
+  }
+}
+
+// One workgroup per chunk, its blocks dealt to its four waves in runs of U.
+template <int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
+__global__ __launch_bounds__(kBlock) void adamw_kernel(AwArgs a) {
+  constexpr int U = 2;
+  const AwChunk ch = a.chunks[blockIdx.x];
+  const Scalars s = scalars(a);
+  if (s.skip) return;
+  const double lr = a.c.lr * ch.lr_scale;
+  const float LR = static_cast<float>(lr), LD = static_cast<float>(lr * ch.decay);
+  const uint32_t lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int full = ch.len / kStateBlock;
+  const int blocks = (ch.len + kStateBlock - 1) / kStateBlock;
+  for (int b = wave * U; b < blocks; b += kWaves * U) {
+    if (b + U <= full) {
+      step_blocks<U, GDT, PDT, BITS, RANDOM, ONE>(a, ch, s.GS, LR, LD, b, lane, -1);
+    } else {
+      for (int k = b; k < b + U && k < blocks; ++k) {
+        int n = ch.len - k * kStateBlock - kQuad * static_cast<int>(lane);
+        n = n < 0 ? 0 : n > kQuad ? kQuad : n;
+        step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, ch, s.GS, LR, LD, k, lane, n);
+      }
+    }
+  }
+}
+
+template <int BITS, bool RANDOM>
+void launch_step(const AwLaunch& L) {
+  with_gdt(L.gdt, [&](auto G) {
+    with_dt(L.pdt, [&](auto H) {
+      constexpr int GDT = decltype(G)::value, PDT = decltype(H)::value;
+      const dim3 grid(static_cast<unsigned>(L.nchunks)), block(kBlock);
+      if (L.a.p == 1)
+        adamw_kernel<GDT, PDT, BITS, RANDOM, true><<<grid, block, 0, L.stream>>>(L.a);
+      else
+        adamw_kernel<GDT, PDT, BITS, RANDOM, false><<<grid, block, 0, L.stream>>>(L.a);
+    });
+  });
+}
+
+}  // namespace
+}  // namespace zs

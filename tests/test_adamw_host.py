@@ -1,0 +1,260 @@
+"""Host-side tests of the AdamW operators' C ABI (no GPU, no kernel launched):
+symbols, sizes, and the refusal of every bad argument before anything reaches
+the device; and the numpy reference that the GPU tests use, against torch."""
+
+import ctypes as C
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+import adamw_ref as ref
+from adam_zs_shard_amd import zsadamw as a
+from adam_zs_shard_amd import zshard as z
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(__file__)), "include", "zsadamw.h")
+FAKE = 1 << 40
+no_device = pytest.mark.skipif(torch.cuda.is_available(),
+                               reason="fake device addresses: CPU-only test")
+
+
+def test_every_declared_symbol_is_exported():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(zs_[a-z_0-9]+)\s*\(", text)))
+    assert names == sorted(a.EXPORTS)
+    for n in names:
+        assert hasattr(a.lib(), n), n
+
+
+def test_workspace_bytes():
+    need = a.zs_adamw_workspace_bytes
+    assert need([], 1) > 0
+    assert need([1], 1) >= 128 + 8
+    # one entry of 128 bytes per 2048 elements at most, one pointer per rank and tensor
+    assert need([5000, 7], 8) - need([5000, 7], 1) >= 0
+    assert need([2048 * 100], 1) >= 100 * 128
+    assert need([10**9], 1) < 10**9 // 8192 * 128 + 4096 * 16
+    for bad in ([0], [-1], [1 << 61], [1 << 59, 1 << 59, 1 << 59]):
+        assert need(bad, 1) == 0
+    assert need([5], 0) == 0 and need([5], z.ZS_MAX_P + 1) == 0
+    assert a.lib().zs_adamw_workspace_bytes(None, 1, 1) == 0
+    # more workgroups than one launch counts
+    assert need([1 << 40], 1) == 0
+
+
+def _piece(i=0, n=1000, p=2, **over):
+    base = FAKE + (i << 34)
+    q = dict(len=n, w=base, m=base + (1 << 30), v=base + (2 << 30), m_scale=base + (3 << 30),
+             v_scale=base + (4 << 30), param=base + (5 << 30), g_mean=base + (6 << 30),
+             grads=[base + (8 << 30) + (r << 28) for r in range(p)], weight_decay=0.1)
+    q.update(over)
+    return q
+
+
+WS = FAKE + (1 << 44)
+
+
+def _upload(pieces, p=2, gdt="bf16", pdt="bf16", bits=32, ws=WS, nbytes=1 << 20):
+    try:
+        a.zs_adamw_upload(pieces, p, gdt, pdt, bits, ws, nbytes, stream=0)
+    except z.ZsError as e:
+        return e.status
+    return z.ZS_OK
+
+
+@no_device
+@pytest.mark.parametrize("over,status", [
+    (dict(len=0), z.ZS_ERR_ARG), (dict(len=-5), z.ZS_ERR_ARG), (dict(len=1 << 61), z.ZS_ERR_ARG),
+    (dict(index=-1), z.ZS_ERR_ARG), (dict(weight_decay=-0.1), z.ZS_ERR_ARG),
+    (dict(weight_decay=float("nan")), z.ZS_ERR_ARG), (dict(lr_scale=float("inf")), z.ZS_ERR_ARG),
+    (dict(w=None), z.ZS_ERR_NULL), (dict(m=None), z.ZS_ERR_NULL), (dict(v=None), z.ZS_ERR_NULL),
+    (dict(param=None), z.ZS_ERR_NULL), (dict(grads=[FAKE, None]), z.ZS_ERR_NULL),
+    (dict(w=FAKE + 2), z.ZS_ERR_ARG), (dict(param=FAKE + (5 << 30) + 1), z.ZS_ERR_ARG),
+    (dict(grads=[FAKE + 1, FAKE + (1 << 28)]), z.ZS_ERR_ARG),
+    (dict(m=FAKE + 3996), z.ZS_ERR_ALIAS),          # the last element of w
+    (dict(param=FAKE + (1 << 30) + 3998), z.ZS_ERR_ALIAS),
+    (dict(g_mean=FAKE + (2 << 30)), z.ZS_ERR_ALIAS),
+    (dict(grads=[FAKE + 2000, FAKE + (9 << 30)]), z.ZS_ERR_ALIAS),
+    (dict(w=WS + 64), z.ZS_ERR_ALIAS),
+])
+def test_upload_refuses_pieces(over, status):
+    assert _upload([_piece(**over)]) == status
+    assert _upload([_piece(1), _piece(**over)]) == status
+
+
+@no_device
+def test_upload_refuses_arguments():
+    q = [_piece()]
+    assert _upload(q, bits=16) == z.ZS_ERR_ARG
+    assert _upload(q, gdt=4) == z.ZS_ERR_DTYPE and _upload(q, pdt=3) == z.ZS_ERR_DTYPE
+    assert _upload(q, ws=None) == z.ZS_ERR_NULL
+    assert _upload(q, ws=WS + 128) == z.ZS_ERR_CAPACITY
+    assert _upload(q, nbytes=a.zs_adamw_workspace_bytes([1000], 2) - 1) == z.ZS_ERR_CAPACITY
+    assert _upload([_piece(m_scale=None)], bits=8) == z.ZS_ERR_NULL
+    assert _upload([_piece(v_scale=None)], bits=8) == z.ZS_ERR_NULL
+    # the fourth scale of m meets v's codes
+    assert _upload([_piece(m_scale=FAKE + (2 << 30) - 12)], bits=8) == z.ZS_ERR_ALIAS
+    assert _upload([_piece(p=0)], p=0) == z.ZS_ERR_ARG
+    many = [_piece(p=z.ZS_MAX_P + 1)]
+    assert _upload(many, p=z.ZS_MAX_P + 1) == z.ZS_ERR_ARG
+    # two tensors that share one gradient may; two that share a weight may not
+    assert _upload([_piece(), _piece(1, w=FAKE)]) == z.ZS_ERR_ALIAS
+    assert _upload([_piece(len=1 << 40)], bits=0) == z.ZS_ERR_RANGE
+    with pytest.raises(ValueError):
+        a.zs_adamw_upload([_piece(p=3)], 2, "bf16", "bf16", 32, WS, 1 << 20, stream=0)
+    assert a.lib().zs_adamw_upload(None, 1, 1, 1, 1, 32, WS, 1 << 20, None,
+                                   C.byref(a.zs_adamw_table())) == z.ZS_ERR_NULL
+
+
+def _table(**over):
+    t = a.zs_adamw_table(WS, 4, 2048, 2, 2, z.ZS_BF16, z.ZS_BF16, 32, 1)
+    for k, x in over.items():
+        setattr(t, k, x)
+    return t
+
+
+HP = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, step=1)
+
+
+@no_device
+@pytest.mark.parametrize("over", [
+    dict(lr=float("nan")), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=float("nan")),
+    dict(eps=float("inf")), dict(eps=-1e-8), dict(step=0), dict(grad_scale=0.0),
+    dict(grad_scale=float("inf")), dict(max_norm=-1.0), dict(max_norm=float("inf")),
+    dict(rounding=2), dict(skip_nonfinite=2)])
+def test_step_refuses_hparams(over):
+    hp = a.hparams(**{**HP, **over})
+    assert a.zs_adamw_step_multi(_table(), hp, FAKE, stream=0, check=False) == z.ZS_ERR_ARG
+
+
+@no_device
+def test_step_and_sumsq_refuse_tables():
+    hp = a.hparams(**HP)
+
+    def step(t, h=hp, sumsq=None):
+        return a.zs_adamw_step_multi(t, h, sumsq, stream=0, check=False)
+
+    def norm(t, sumsq=FAKE, **k):
+        return a.zs_grad_sumsq_multi(t, sumsq, stream=0, check=False, **k)
+
+    for over, st in ((dict(workspace=None), z.ZS_ERR_NULL), (dict(p=0), z.ZS_ERR_ARG),
+                     (dict(p=z.ZS_MAX_P + 1), z.ZS_ERR_ARG), (dict(npieces=-1), z.ZS_ERR_ARG),
+                     (dict(nchunks=1), z.ZS_ERR_ARG), (dict(nchunks=1 << 24), z.ZS_ERR_ARG),
+                     (dict(chunk_elems=100), z.ZS_ERR_ARG), (dict(state_bits=16), z.ZS_ERR_ARG),
+                     (dict(grad_dtype=4), z.ZS_ERR_DTYPE), (dict(param_dtype=3), z.ZS_ERR_DTYPE)):
+        assert step(_table(**over)) == st and norm(_table(**over)) == st, over
+    assert step(_table(state_bits=0)) == z.ZS_ERR_ARG
+    assert step(_table(), a.hparams(**HP, max_norm=1.0)) == z.ZS_ERR_NULL
+    assert step(_table(), a.hparams(**HP, skip_nonfinite=True)) == z.ZS_ERR_NULL
+    assert step(_table(), a.hparams(**HP, max_norm=1.0), FAKE + 4) == z.ZS_ERR_ARG
+    assert a.lib().zs_adamw_step_multi(None, C.byref(hp), None, None) == z.ZS_ERR_NULL
+    assert a.lib().zs_adamw_step_multi(C.byref(_table()), None, None, None) == z.ZS_ERR_NULL
+    assert norm(_table(), None) == z.ZS_ERR_NULL and norm(_table(), FAKE + 4) == z.ZS_ERR_ARG
+    assert norm(_table(has_mean=0), store_mean=True) == z.ZS_ERR_NULL
+    assert norm(_table(), store_mean=2) == z.ZS_ERR_ARG
+    assert norm(_table(), accumulate=2) == z.ZS_ERR_ARG
+    # a step over no tensors is no launch
+    assert step(_table(nchunks=0, npieces=0)) == z.ZS_OK
+
+
+@no_device
+def test_convert_refuses():
+    x, c, s = FAKE, FAKE + (1 << 30), FAKE + (2 << 30)
+    for enc in (True, False):
+        def call(x=x, n=1000, kind="m", c=c, s=s):
+            if enc:
+                return a.zs_state8_encode(x, n, kind, c, s, stream=0, check=False)
+            return a.zs_state8_decode(c, s, n, kind, x, stream=0, check=False)
+
+        assert call(n=0) == z.ZS_OK and call(n=-1) == z.ZS_ERR_ARG
+        assert call(n=1 << 61) == z.ZS_ERR_RANGE and call(kind=2) == z.ZS_ERR_ARG
+        assert call(x=None) == call(c=None) == call(s=None) == z.ZS_ERR_NULL
+        assert call(x=x + 2) == call(s=s + 1) == z.ZS_ERR_ARG
+        assert call(c=x + 3999) == call(s=c + 996) == call(s=x) == z.ZS_ERR_ALIAS
+
+
+# ---- the reference itself -------------------------------------------------------
+@pytest.mark.parametrize("kind,dtype", [("m", torch.float8_e4m3fn), ("v", torch.float8_e5m2)])
+def test_reference_grid_is_the_types(kind, dtype):
+    t = torch.arange(256, dtype=torch.uint8).view(dtype).float().numpy()
+    assert np.array_equal(ref.grid_values(kind).astype(np.float32), t, equal_nan=True)
+    x = np.random.default_rng(1).standard_normal(40_000).astype(np.float32) ** 3
+    x = np.abs(x) if kind == "v" else x
+    codes, scales = ref.encode(x, kind)
+    pad = np.zeros(-(-x.size // 256) * 256, np.float32)
+    pad[:x.size] = x
+    most = np.abs(pad.reshape(-1, 256)).max(1, keepdims=True)
+    y = torch.from_numpy(np.minimum(pad.reshape(-1, 256) * (np.float32(ref.TOP[kind]) / most),
+                                    np.float32(ref.TOP[kind]))).to(dtype)
+    same = y.view(torch.uint8).numpy().reshape(-1)[:x.size] == codes
+    assert np.all(same | ((codes == 1) & (kind == "v")))
+    # a value is off by half its grid's spacing at most, plus the two products' roundings
+    bound = 2.0 ** -(ref.BITS[kind] + 1) + 4 * ref.U
+    big = np.abs(pad.reshape(-1, 256)) >= most * 2.0 ** (ref.LEAST[kind] - 8 + (kind == "v") * -7)
+    back = ref.decode(codes, scales, kind)
+    sel = big.reshape(-1)[:x.size] & (x != 0)
+    assert np.all(np.abs(back[sel] - x[sel]) <= bound * np.abs(x[sel]))
+
+
+def test_reference_philox_known_answers():
+    # seven rounds by hand on Python integers
+    def one(c, k):
+        for _ in range(7):
+            x, y = c[0] * 0xD2511F53, c[2] * 0xCD9E8D57
+            c = [(y >> 32) ^ c[1] ^ k[0], y & 0xFFFFFFFF, (x >> 32) ^ c[3] ^ k[1], x & 0xFFFFFFFF]
+            k = [(k[0] + 0x9E3779B9) % 2**32, (k[1] + 0xBB67AE85) % 2**32]
+        return c
+
+    seed, step = 0x123456789ABCDEF0, (3 << 32) + 7
+    idx = np.array([0, 4, (5 << 32) + 8], np.uint64)
+    got = ref.philox(idx, step, seed)
+    for i, row in zip(idx.tolist(), got):
+        want = one([i & 0xFFFFFFFF, i >> 32, step & 0xFFFFFFFF, step >> 32],
+                   [seed & 0xFFFFFFFF, seed >> 32])
+        assert [int(x) for x in row] == want
+
+
+def test_reference_random_rounding_keeps_the_mean():
+    """All 2^16 random halves of a value: the mean stored is the value to the
+    16 bits' own half step, 2^-17 of the grid's spacing."""
+    halves = np.arange(1 << 16, dtype=np.uint32)
+    for kind in ("m", "v"):
+        for x in (1.07, 0.3, 2.0 ** -9, 3.3e-5):
+            row = np.full(256, x, np.float32)
+            row[0] = 1.0 if x < 1 else x  # the block's largest value
+            mean = 0.0
+            for k in range(0, 1 << 16, 255):
+                h = np.zeros(256, np.uint32)
+                part = halves[k:k + 255]
+                h[1:1 + part.size] = part
+                c, s = ref.encode(row, kind, h)
+                mean += ref.decode(c, s, kind)[1:1 + part.size].astype(np.float64).sum()
+            mean /= 1 << 16
+            top = float(row[0])
+            spacing = max(2.0 ** -ref.BITS[kind] * x, top / ref.TOP[kind] * 2.0 ** (ref.LEAST[kind] - ref.BITS[kind]))
+            assert abs(mean - x) <= spacing * (2.0 ** -17 + 2.0 ** -16) + 8 * ref.U * x, (kind, x)
+
+
+def test_reference_step_is_torch_adamw():
+    rng = np.random.default_rng(3)
+    n, t0 = 4000, 1
+    w = rng.standard_normal(n).astype(np.float32) * 0.02
+    p = torch.nn.Parameter(torch.from_numpy(w.astype(np.float64)))
+    opt = torch.optim.AdamW([p], lr=1e-3, betas=(0.9, 0.95), eps=1e-8, weight_decay=0.1)
+    m = np.zeros(n, np.float32)
+    v = np.zeros(n, np.float32)
+    m64, v64, w64 = (x.astype(np.float64) for x in (m, v, w))
+    slack = np.zeros(n)
+    for t in range(t0, t0 + 6):
+        g = rng.standard_normal(n).astype(np.float32)
+        p.grad = torch.from_numpy(g.astype(np.float64))
+        opt.step()
+        h = dict(lr=1e-3, decay=0.1, beta1=0.9, beta2=0.95, eps=1e-8, step=t, gs=1.0)
+        w64, m64, v64, bw, _, _ = ref.step64([g], w64, m64, v64, h)
+        w, m, v = ref.step32(g, w, m, v, h)
+        slack += bw + 1e-3 * 1e-5  # what earlier steps' roundings of m and v do to this one's quotient
+        # torch decays first and moves then: lr^2 * decay * u apart
+        assert np.all(np.abs(p.detach().numpy() - w64) <= t * 1e-3 * 1e-3 * 0.1 * 12)
+        assert np.all(np.abs(w - w64) <= slack)

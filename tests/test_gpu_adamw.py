@@ -1,0 +1,564 @@
+"""The AdamW operators on the GPU against the numpy references of adamw_ref: bit
+for bit with the stated fp32 sequence, and within the bounds that adamw_ref
+derives of the definition in 64 bits."""
+
+import numpy as np
+import pytest
+import torch
+
+import adamw_ref as ref
+from adam_zs_shard_amd import zsadamw as a
+from adam_zs_shard_amd import zshard as z
+from gpu_util import DEV, need_gpu
+
+pytestmark = pytest.mark.gpu
+TD = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+GAP = 40  # elements between two tensors' buffers, which nothing may write
+CANARY = {4: 0x5A5A5A5A, 2: 0x5A5A, 1: 0x5A}
+LR, B1, B2, EPS = 3e-4, 0.9, 0.95, 1e-8
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    need_gpu()
+    yield
+    torch.cuda.synchronize()
+
+
+def bits_of(x):
+    x = x.detach().contiguous().cpu()
+    return x.view({4: torch.int32, 2: torch.int16, 1: torch.uint8, 8: torch.int64}[x.element_size()]
+                  ).numpy()
+
+
+def same(got, want, what):
+    g, w = bits_of(got), np.ascontiguousarray(want).view({4: np.int32, 2: np.int16, 1: np.uint8}[
+        want.dtype.itemsize])
+    if want.dtype.kind == "f":
+        nan = np.isnan(want)
+        assert np.array_equal(nan, np.isnan(got.detach().float().cpu().numpy())), what
+        g, w = g[~nan], w[~nan]
+    assert g.shape == w.shape and np.array_equal(g, w), \
+        f"{what}: {int((g != w).sum())} of {w.size} differ in bits"
+
+
+class Buffers:
+    """Many tensors in one allocation per kind, GAP canaries between them, the
+    first one `shift` elements in."""
+
+    def __init__(self, lens, dtype, shift):
+        self.lens, self.dtype = lens, dtype
+        size = torch.empty(0, dtype=dtype).element_size()
+        self.offs, at = [], shift + GAP
+        for n in lens:
+            self.offs.append(at)
+            at += n + GAP
+        raw = {4: torch.int32, 2: torch.int16, 1: torch.uint8}[size]
+        self.flat = torch.full((at,), CANARY[size], dtype=raw, device=DEV).view(dtype)
+        self.canary = torch.ones(at, dtype=torch.bool, device=DEV)
+        for n, o in zip(lens, self.offs):
+            self.canary[o:o + n] = False
+        self.raw, self.size = raw, size
+
+    def __getitem__(self, i):
+        return self.flat[self.offs[i]:self.offs[i] + self.lens[i]]
+
+    def fill(self, arrays):
+        for i, x in enumerate(arrays):
+            self[i].copy_(x if isinstance(x, torch.Tensor) else torch.from_numpy(x))
+        return self
+
+    def check(self, what):
+        assert bool((self.flat.view(self.raw)[self.canary] == CANARY[self.size]).all()), \
+            f"{what}: written outside its tensors"
+
+
+class Model:
+    def __init__(self, lens, p=1, grad="bf16", param="bf16", bits=32, shift=0, seed=0, states=True,
+                 mean=False, gscale=1e-3):
+        self.lens, self.p, self.grad, self.param, self.bits = lens, p, grad, param, bits
+        r = self.rng = np.random.default_rng(seed)
+        nb = [-(-n // 256) for n in lens]
+        self.decay = [0.1 if n > 300 else 0.0 for n in lens]
+        self.lr_scale = [[1.0, 0.5, 2.0][i % 3] for i in range(len(lens))]
+        self.index = [int(x) for x in r.integers(0, 1 << 40, len(lens))]
+        self.gscale = gscale
+        self.g = [Buffers(lens, TD[grad], shift) for _ in range(p)]
+        self.draw()
+        w = [r.standard_normal(n).astype(np.float32) * np.float32(0.02) for n in lens]
+        m = [r.standard_normal(n).astype(np.float32) * np.float32(3e-4) for n in lens]
+        v = [(np.abs(r.standard_normal(n)).astype(np.float32) + np.float32(0.1)) ** 2 *
+             np.float32(1e-6) for n in lens]
+        if not states:
+            m, v = [np.zeros_like(x) for x in m], [np.zeros_like(x) for x in v]
+        self.w = Buffers(lens, torch.float32, shift).fill(w)
+        self.pb = Buffers(lens, TD[param], shift) if param else None
+        if bits == 8:
+            cm, cv = [ref.encode(x, "m") for x in m], [ref.encode(x, "v") for x in v]
+            self.m = Buffers(lens, torch.uint8, shift).fill([c for c, _ in cm])
+            self.v = Buffers(lens, torch.uint8, shift).fill([c for c, _ in cv])
+            self.ms = Buffers(nb, torch.float32, shift).fill([s for _, s in cm])
+            self.vs = Buffers(nb, torch.float32, shift).fill([s for _, s in cv])
+        else:
+            self.m = Buffers(lens, torch.float32, shift).fill(m)
+            self.v = Buffers(lens, torch.float32, shift).fill(v)
+        self.mean = Buffers(lens, torch.float32, shift) if mean else None
+        self.table = self.upload()
+
+    def draw(self):
+        """New gradients, some of them zero."""
+        for b in self.g:
+            xs = []
+            for n in self.lens:
+                x = self.rng.standard_normal(n).astype(np.float32) * np.float32(self.gscale)
+                x[self.rng.random(n) < 0.05] = 0
+                xs.append(x)
+            b.fill(xs)
+
+    def pieces(self):
+        out = []
+        for i, n in enumerate(self.lens):
+            q = dict(len=n, grads=[b[i] for b in self.g], w=self.w[i], m=self.m[i], v=self.v[i],
+                     weight_decay=self.decay[i], lr_scale=self.lr_scale[i], index=self.index[i])
+            if self.pb:
+                q["param"] = self.pb[i]
+            if self.bits == 8:
+                q.update(m_scale=self.ms[i], v_scale=self.vs[i])
+            if self.mean:
+                q["g_mean"] = self.mean[i]
+            out.append(q)
+        return out
+
+    def upload(self):
+        nb = a.zs_adamw_workspace_bytes(self.lens, self.p)
+        self.ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+        return a.zs_adamw_upload(self.pieces(), self.p, self.grad, self.param, self.bits, self.ws, nb)
+
+    def host(self, i):
+        d = dict(g=[b[i].float().cpu().numpy() for b in self.g], w=self.w[i].cpu().numpy().copy())
+        for k in "mv":
+            x = getattr(self, k)[i].cpu().numpy().copy()
+            if self.bits == 8:
+                d["c" + k], d["s" + k] = x, getattr(self, k + "s")[i].cpu().numpy().copy()
+                x = ref.decode(x, d["s" + k], k)
+            d[k] = x
+        return d
+
+    def all(self):
+        bufs = [self.w, self.m, self.v] + ([self.pb] if self.pb else [])
+        return bufs + ([self.ms, self.vs] if self.bits == 8 else [])
+
+    def step_and_check(self, step, *, grad_scale=1.0, sumsq=None, max_norm=0.0, rounding="nearest",
+                       seed=0, bounds=True, run=None):
+        before = [self.host(i) for i in range(len(self.lens))]
+        hp = a.hparams(LR, B1, B2, EPS, step, grad_scale=grad_scale, max_norm=max_norm,
+                       rounding=rounding, seed=seed)
+        dev = None if sumsq is None else torch.tensor(sumsq, dtype=torch.float64, device=DEV)
+        (run or a.zs_adamw_step_multi)(self.table, hp, dev)
+        gs, _ = ref.scale_of(grad_scale, sumsq, max_norm)
+        for i, (n, d) in enumerate(zip(self.lens, before)):
+            h = dict(lr=LR * self.lr_scale[i], decay=self.decay[i], beta1=B1, beta2=B2, eps=EPS,
+                     step=step, gs=gs)
+            w, m, v = ref.step32(ref.mean32(d["g"]), d["w"], d["m"], d["v"], h, self.bits)
+            what = f"tensor {i} of {n}"
+            same(self.w[i], w, what + " w")
+            if self.pb:  # a NaN is a NaN, whatever its bits
+                fine = ~np.isnan(w)
+                assert np.array_equal(fine, ~np.isnan(self.pb[i].float().cpu().numpy()))
+                same(self.pb[i][torch.from_numpy(fine).to(DEV)],
+                     torch.from_numpy(w[fine]).to(TD[self.param]).view(torch.int16).numpy(),
+                     what + " param")
+            if self.bits == 32:
+                same(self.m[i], m, what + " m")
+                same(self.v[i], v, what + " v")
+            else:
+                lo = hi = None
+                if rounding == "stochastic":
+                    lo, hi = ref.halves_for(n, self.index[i], step, seed)
+                for k, x, r in (("m", m, lo), ("v", v, hi)):
+                    codes, scales = ref.encode(x, k, r)
+                    same(getattr(self, k)[i], codes, what + f" {k} codes")
+                    same(getattr(self, k + "s")[i], scales, what + f" {k} scales")
+            if bounds and n >= 1:
+                w64, m64, v64, bw, bm, bv = ref.step64(d["g"], d["w"], d["m"], d["v"], h)
+                # the 8-bit form multiplies by rounded reciprocals where the other divides
+                assert np.all(np.abs(self.w[i].cpu().numpy() - w64) <= bw * (1 if self.bits == 32 else 1.5))
+                if self.bits == 32:
+                    assert np.all(np.abs(self.m[i].cpu().numpy() - m64) <= bm)
+                    assert np.all(np.abs(self.v[i].cpu().numpy() - v64) <= bv)
+        for b in self.all() + self.g:
+            b.check("buffer")
+
+
+ODD = [1, 2, 3, 255, 256, 257, 1000, 2047, 2048, 2049, 5, 8192, 8195, 30011]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("grad,param,p,shift", [
+    ("bf16", "bf16", 1, 0), ("f16", "f16", 1, 1), ("f32", "bf16", 1, 0), ("f32", None, 3, 3),
+    ("bf16", "f16", 2, 8), ("bf16", None, 5, 2), ("f16", "bf16", 8, 0), ("f16", "f16", 7, 13)])
+def test_step_of_odd_tensors(bits, grad, param, p, shift):
+    M = Model(ODD, p, grad, param, bits, shift, seed=10 + p)
+    M.step_and_check(1)
+    M.draw()
+    M.step_and_check(1000, grad_scale=0.25)
+
+
+@pytest.mark.parametrize("bits,rounding", [(32, "nearest"), (8, "nearest"), (8, "stochastic")])
+@pytest.mark.parametrize("p", [1, 4])
+def test_step_of_large_tensors(bits, rounding, p):
+    # enough for the larger workgroups, pieces that end inside one
+    M = Model([3_000_001, 513, 1_300_000, 77], p, "bf16", "bf16", bits, seed=20)
+    M.step_and_check(17, rounding=rounding, seed=(7 << 32) + 5)
+
+
+@pytest.mark.parametrize("grad", ["f16", "f32"])
+def test_step_of_many_ranks(grad):
+    M = Model([2500, 3], 300, grad, "bf16", 32, seed=3)
+    M.step_and_check(2)
+
+
+@pytest.mark.parametrize("shift", [0, 1, 2, 5, 8])
+def test_stochastic_rounding_bits(shift):
+    M = Model(ODD, 2, "bf16", "bf16", 8, shift, seed=31)
+    for step, seed in ((1, 0), (2, 2**64 - 1), ((1 << 33) + 1, 12345678901234567)):
+        M.draw()
+        M.step_and_check(step, rounding="stochastic", seed=seed)
+
+
+def test_no_decay_no_clip_is_the_adam_step():
+    """Bit for bit with zs_fused_shard_step_multi where decay and clipping are off."""
+    lens = [5000, 1, 70_001]
+    M = Model(lens, 4, "bf16", "bf16", 32, seed=5)
+    M.decay, M.lr_scale = [0.0] * 3, [1.0] * 3
+    M.table = M.upload()
+    other = [Buffers(lens, torch.float32, 0).fill([x[i].clone() for i in range(3)])
+             for x in (M.w, M.m, M.v)]
+    par = Buffers(lens, torch.bfloat16, 0)
+    chunk = 2048
+    pieces = [(i, 0, sum(lens[:i]), n) for i, n in enumerate(lens)]
+    nb = z.zs_mt_workspace_bytes(3, sum(-(-n // chunk) for n in lens), 4)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    ptrs = [dict(w=other[0][i], m=other[1][i], v=other[2][i], param=par[i],
+                 grads=[b[i] for b in M.g]) for i in range(3)]
+    t = z.zs_mt_upload(pieces, ptrs, 4, "bf16", "bf16", chunk, ws, nb)
+    for step in (1, 2, 3):
+        z.zs_fused_shard_step_multi(t, z.hparams(LR, B1, B2, EPS, step))
+        a.zs_adamw_step_multi(M.table, a.hparams(LR, B1, B2, EPS, step))
+    for i in range(3):
+        for x, y in zip((M.w, M.m, M.v, M.pb), other + [par]):
+            assert np.array_equal(bits_of(x[i]), bits_of(y[i]))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("grad_scale,sumsq,max_norm", [
+    (1.0, 9.0, 1.0),              # clipped to a third
+    (1.0, 0.25, 1.0),             # below the limit
+    (1.0, 0.0, 1.0),
+    (1.0, 4.0, 0.0),              # a norm that nothing uses
+    (1 / 1024, 25.0 * 2 ** 20, 2.0),
+    (-2.0, 9.0, 1.0),
+])
+def test_clipping(bits, grad_scale, sumsq, max_norm):
+    M = Model([3000, 300], 1, "bf16", "bf16", bits, seed=6)
+    M.step_and_check(3, grad_scale=grad_scale, sumsq=sumsq, max_norm=max_norm)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_nonfinite_norm(bits, bad):
+    M = Model([3000, 300], 1, "bf16", "bf16", bits, seed=6)
+    before = [b.flat.clone() for b in M.all()]
+    sumsq = torch.tensor(bad, dtype=torch.float64, device=DEV)
+    hp = a.hparams(LR, B1, B2, EPS, 3, max_norm=1.0, skip_nonfinite=True)
+    a.zs_adamw_step_multi(M.table, hp, sumsq)
+    for b, x in zip(M.all(), before):
+        assert np.array_equal(bits_of(b.flat), bits_of(x))
+    # a finite one does step
+    sumsq.fill_(4.0)
+    a.zs_adamw_step_multi(M.table, hp, sumsq)
+    assert not np.array_equal(bits_of(M.w.flat), bits_of(before[0]))
+    # without the switch an infinite norm scales the gradient to zero, NaN poisons
+    M = Model([3000, 300], 1, "bf16", "bf16", bits, seed=6)
+    if bad == float("inf"):
+        M.step_and_check(3, sumsq=bad, max_norm=1.0, bounds=False)
+    else:
+        a.zs_adamw_step_multi(M.table, a.hparams(LR, B1, B2, EPS, 3, max_norm=1.0),
+                              torch.tensor(bad, dtype=torch.float64, device=DEV))
+        assert bool(M.w[0].isnan().all())
+
+
+@pytest.mark.parametrize("rounding", ["nearest", "stochastic"])
+def test_8bit_blocks_with_special_values(rounding):
+    lens = [256 * 6 + 10]
+    M = Model(lens, 1, "f32", "bf16", 8, seed=8)
+    g = M.g[0][0]
+    M.m[0].zero_(), M.v[0].zero_(), M.ms[0].zero_(), M.vs[0].zero_()
+    g[:256] = 0                       # nothing seen, nothing held
+    g[256:512] = 1e-35                # below what a block holds: zeros
+    g[300] = -1e-36
+    g[512:768] *= torch.logspace(-20, 3, 256, device=DEV)   # over the whole range of codes
+    g[768] = float("inf")
+    g[1024 + 7] = float("nan")
+    g[1280:1536] = 1e-20              # v underflows to zero
+    g[1280] = 1e-3
+    g[-3:] = 0
+    M.step_and_check(1, rounding=rounding, seed=3, bounds=False)
+    s = M.ms[0].cpu().numpy()
+    assert s[0] == 0 and s[1] == 0 and np.isnan(s[3]) and np.isnan(s[4]) and s[5] > 0
+    v = ref.decode(M.v[0].cpu().numpy(), M.vs[0].cpu().numpy(), "v")
+    gh = g.cpu().numpy()
+    seen = (gh != 0) & (np.float32(1 - B2) * (gh * gh) > 0) & np.isfinite(v)
+    seen[256:512] = False
+    assert np.all(v[seen] > 0)        # a positive v stays one
+
+
+def test_stochastic_rounding_keeps_the_mean_over_steps():
+    """Unbiased over seeds: 5 standard deviations of a rounding that is off by
+    one spacing at most."""
+    n, seeds = 4096, 64
+    M = Model([n], 1, "bf16", None, 8, seed=9)
+    keep = [b.flat.clone() for b in M.all()]
+    d = M.host(0)
+    h = dict(lr=LR, decay=0.1, beta1=B1, beta2=B2, eps=EPS, step=5, gs=1.0)
+    _, m, v = ref.step32(ref.mean32(d["g"]), d["w"], d["m"], d["v"], h, 8)
+    sums = {"m": 0.0, "v": 0.0}
+    for seed in range(seeds):
+        for b, x in zip(M.all(), keep):
+            b.flat.copy_(x)
+        a.zs_adamw_step_multi(M.table, a.hparams(LR, B1, B2, EPS, 5, rounding="stochastic", seed=seed))
+        for k in sums:
+            sums[k] = sums[k] + M.host(0)[k].astype(np.float64)
+    for k, x in (("m", m), ("v", v)):
+        top = np.repeat(np.abs(x).reshape(-1, 256).max(1), 256)
+        spacing = np.maximum(np.abs(x) * 2.0 ** -ref.BITS[k],
+                             top / ref.TOP[k] * 2.0 ** (ref.LEAST[k] - ref.BITS[k]))
+        off = (sums[k] / seeds - x) / spacing
+        # the mean over all values of a difference whose deviation is at most 1/2 each
+        assert abs(off.mean()) <= 5 * 0.5 / np.sqrt(n * seeds), k
+        assert np.abs(off).max() <= 6 * 0.5 / np.sqrt(seeds), k
+
+
+# ---- the norm ---------------------------------------------------------------------
+@pytest.mark.parametrize("grad,p,shift,store", [
+    ("bf16", 1, 0, False), ("f16", 1, 1, True), ("f32", 1, 0, False), ("f32", 3, 1, True),
+    ("bf16", 8, 0, True), ("f16", 5, 3, False), ("bf16", 300, 0, True)])
+def test_sumsq(grad, p, shift, store):
+    lens = ODD + ([3_000_001, 1_200_003] if p < 9 else [])
+    M = Model(lens, p, grad, None, 32, shift, seed=40 + p, mean=store, gscale=1e-2)
+    out = torch.full((3,), 7.0, dtype=torch.float64, device=DEV)
+    a.zs_grad_sumsq_multi(M.table, out[1:], store_mean=store)
+    means = [ref.mean32([b[i].float().cpu().numpy() for b in M.g]) for i in range(len(lens))]
+    want = sum(float(np.dot(x.astype(np.float64), x.astype(np.float64))) for x in means)
+    got = out.cpu().numpy()
+    assert got[0] == 7.0 and got[2] == 7.0
+    # both sums in double over positive terms: at most n roundings of half a step each, in fact far fewer
+    assert abs(got[1] - want) <= sum(lens) * 2.0 ** -53 * want
+    if store:
+        for i, x in enumerate(means):
+            same(M.mean[i], x, f"mean of tensor {i}")
+        M.mean.check("mean")
+    for b in M.g + M.all():
+        b.check("buffer")
+    # the same bits again; and added to what is there
+    again = torch.zeros((), dtype=torch.float64, device=DEV)
+    a.zs_grad_sumsq_multi(M.table, again)
+    assert again.item() == got[1]
+    a.zs_grad_sumsq_multi(M.table, again, accumulate=True)
+    assert again.item() == got[1] + got[1]
+
+
+@pytest.mark.parametrize("value,want", [(float("inf"), float("inf")), (float("nan"), float("nan")),
+                                        (3e38, 9e76 * 5)])
+def test_sumsq_of_large_and_nonfinite(value, want):
+    M = Model([1000], 1, "f32", None, 32, seed=1)
+    M.g[0][0].zero_()
+    M.g[0][0][::200] = value
+    out = torch.zeros((), dtype=torch.float64, device=DEV)
+    a.zs_grad_sumsq_multi(M.table, out)
+    assert out.isnan().item() if np.isnan(want) else out.item() == pytest.approx(want, rel=2.0 ** -23)
+
+
+def test_sumsq_of_no_tensors():
+    ws = torch.empty(a.zs_adamw_workspace_bytes([], 1), dtype=torch.uint8, device=DEV)
+    t = a.zs_adamw_upload([], 1, "bf16", "bf16", 32, ws, ws.numel())
+    out = torch.full((), 5.0, dtype=torch.float64, device=DEV)
+    a.zs_grad_sumsq_multi(t, out, accumulate=True)
+    assert out.item() == 5.0
+    a.zs_grad_sumsq_multi(t, out)
+    assert out.item() == 0.0
+    a.zs_adamw_step_multi(t, a.hparams(LR, B1, B2, EPS, 1))
+
+
+# ---- conversions ------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ["m", "v"])
+def test_every_code_decodes_and_encodes(kind):
+    codes = torch.arange(256, dtype=torch.uint8, device=DEV)
+    dtype = torch.float8_e4m3fn if kind == "m" else torch.float8_e5m2
+    for s in (1.0, 3.7e-9, 2.0 ** -100):
+        scale = torch.full((1,), s, device=DEV)
+        x = torch.empty(256, device=DEV)
+        a.zs_state8_decode(codes, scale, 256, kind, x)
+        same(x, ref.decode(codes.cpu().numpy(), np.full(1, s, np.float32), kind), f"scale {s}")
+    # values on the grid and the midpoints between them, the largest present: ties to even
+    grid = ref.grid_values(kind)[:128]
+    grid = grid[np.isfinite(grid)]
+    mid = (grid[1:] + grid[:-1]) / 2
+    for vals in (grid, mid, np.nextafter(mid, np.inf), np.nextafter(mid, 0)):
+        x = np.zeros(256, np.float32)
+        x[:vals.size] = vals
+        x[255] = ref.TOP[kind]
+        if kind == "m":
+            x[1:vals.size:2] *= -1
+        got = torch.empty(256, dtype=torch.uint8, device=DEV)
+        sc = torch.empty(1, device=DEV)
+        a.zs_state8_encode(torch.from_numpy(x).to(DEV), 256, kind, got, sc)
+        c, s = ref.encode(x, kind)
+        same(got, c, "codes")
+        same(sc, s, "scale")
+        if kind == "m" or vals is grid:
+            t = torch.from_numpy(x).to(dtype).view(torch.uint8).numpy()
+            assert np.array_equal(t, c)
+
+
+@pytest.mark.parametrize("kind", ["m", "v"])
+@pytest.mark.parametrize("n", [1, 3, 255, 256, 257, 4097, 1_000_003])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_convert(kind, n, shift):
+    r = np.random.default_rng(n)
+    x = (r.standard_normal(n) * 10.0 ** r.uniform(-6, 1, n)).astype(np.float32)
+    x = np.abs(x) if kind == "v" else x
+    src = Buffers([n], torch.float32, shift).fill([x])
+    codes = Buffers([n], torch.uint8, shift)
+    sc = Buffers([-(-n // 256)], torch.float32, 0)
+    back = Buffers([n], torch.float32, shift)
+    a.zs_state8_encode(src[0], n, kind, codes[0], sc[0])
+    a.zs_state8_decode(codes[0], sc[0], n, kind, back[0])
+    c, s = ref.encode(x, kind)
+    same(codes[0], c, "codes")
+    same(sc[0], s, "scales")
+    same(back[0], ref.decode(c, s, kind), "values")
+    for b in (src, codes, sc, back):
+        b.check("buffer")
+
+
+# ---- together, on streams and in graphs ---------------------------------------------
+@pytest.mark.parametrize("bits,rounding", [(32, "nearest"), (8, "stochastic")])
+def test_training_steps_with_clipping(bits, rounding):
+    """Norm over two tables (the mean of 4 ranks kept), then the steps from the
+    stored mean, three times over."""
+    lens = [3000, 500, 70_003]
+    M = Model(lens, 1, "f32", "bf16", bits, seed=50, states=False)
+    R = [Model(lens[i:j], 4, "bf16", None, 32, seed=51 + i, mean=True) for i, j in ((0, 2), (2, 3))]
+    for i in range(3):
+        M.g[0].offs  # the step's gradients are the norm's means
+    src = [R[0].mean[0], R[0].mean[1], R[1].mean[0]]
+    ps = M.pieces()
+    for q, x in zip(ps, src):
+        q["grads"] = [x]
+    M.table = a.zs_adamw_upload(ps, 1, "f32", "bf16", bits, M.ws, M.ws.numel())
+    sumsq = torch.zeros((), dtype=torch.float64, device=DEV)
+    for step in (1, 2, 3):
+        for k, r in enumerate(R):
+            r.draw()
+            a.zs_grad_sumsq_multi(r.table, sumsq, store_mean=True, accumulate=k > 0)
+        for i, x in enumerate(src):
+            M.g[0][i].copy_(x)
+        M.step_and_check(step, sumsq=sumsq.item(), max_norm=0.1, rounding=rounding, seed=4)
+        assert sumsq.item() > 0.01  # it did clip
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_and_replayed(bits):
+    """A captured norm and step, replayed with eager work between, against the
+    eager calls: every replay."""
+    M, E = (Model([5000, 300, 30_001], 2, "bf16", "bf16", bits, seed=60, mean=True) for _ in range(2))
+    sums = [torch.zeros((), dtype=torch.float64, device=DEV) for _ in range(2)]
+    hp = a.hparams(LR, B1, B2, EPS, 9, max_norm=0.05, rounding="stochastic" if bits == 8 else "nearest",
+                   seed=77)
+
+    def both(x, out):
+        a.zs_grad_sumsq_multi(x.table, out, store_mean=True)
+        a.zs_adamw_step_multi(x.table, hp, out)
+
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph):
+            both(M, sums[0])
+    torch.cuda.current_stream().wait_stream(side)
+    for _ in range(4):
+        E.draw()
+        for x, y in zip(M.g, E.g):
+            x.flat.copy_(y.flat)
+        graph.replay()
+        both(E, sums[1])
+        torch.cuda.synchronize()
+        assert sums[0].item() == sums[1].item()
+        for x, y in zip(M.all() + [M.mean], E.all() + [E.mean]):
+            assert np.array_equal(bits_of(x.flat), bits_of(y.flat))
+
+
+def test_two_streams_at_once():
+    M = [Model([200_003, 5000], 1, "bf16", "bf16", 8, seed=70 + i) for i in range(2)]
+    E = [Model([200_003, 5000], 1, "bf16", "bf16", 8, seed=70 + i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in M]
+    sums = torch.zeros(2, dtype=torch.float64, device=DEV)
+    for step in range(1, 6):
+        hp = a.hparams(LR, B1, B2, EPS, step, max_norm=1.0)
+        for i, (m, s) in enumerate(zip(M, streams)):
+            s.wait_stream(torch.cuda.current_stream())
+            a.zs_grad_sumsq_multi(m.table, sums[i], stream=s)
+            a.zs_adamw_step_multi(m.table, hp, sums[i], stream=s)
+    torch.cuda.synchronize()
+    one = torch.zeros((), dtype=torch.float64, device=DEV)
+    for m, e in zip(M, E):
+        for step in range(1, 6):
+            a.zs_grad_sumsq_multi(e.table, one)
+            a.zs_adamw_step_multi(e.table, a.hparams(LR, B1, B2, EPS, step, max_norm=1.0), one)
+        for x, y in zip(m.all(), e.all()):
+            assert np.array_equal(bits_of(x.flat), bits_of(y.flat))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_offsets_beyond_32_bits(bits):
+    """One tensor of 1.1e9 elements: its first and last blocks."""
+    n = 1_100_000_123
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(2)
+    g = torch.randn(n, generator=gen, device=DEV, dtype=torch.bfloat16).mul_(1e-3)
+    w = torch.randn(n, generator=gen, device=DEV).mul_(0.02)
+    sd = torch.uint8 if bits == 8 else torch.float32
+    m, v = torch.zeros(n, dtype=sd, device=DEV), torch.zeros(n, dtype=sd, device=DEV)
+    nb = -(-n // 256)
+    ms, vs = torch.zeros(nb, device=DEV), torch.zeros(nb, device=DEV)
+    par = torch.zeros(n, dtype=torch.bfloat16, device=DEV)
+    ws = torch.empty(a.zs_adamw_workspace_bytes([n], 1), dtype=torch.uint8, device=DEV)
+    index = (1 << 40) + 5
+    t = a.zs_adamw_upload([dict(len=n, grads=[g], w=w, m=m, v=v, m_scale=ms, v_scale=vs, param=par,
+                                weight_decay=0.1, index=index)], 1, "bf16", "bf16", bits, ws, ws.numel())
+    parts = [(0, 4096), (n // 2 // 256 * 256, 4096), (n // 256 * 256 - 2048, 2048 + n % 256)]
+    w0 = [w[o:o + k].cpu().numpy().copy() for o, k in parts]
+    a.zs_adamw_step_multi(t, a.hparams(LR, B1, B2, EPS, 1, rounding="stochastic", seed=1))
+    h = dict(lr=LR, decay=0.1, beta1=B1, beta2=B2, eps=EPS, step=1, gs=1.0)
+    for (o, k), x in zip(parts, w0):
+        zero = np.zeros(k, np.float32)
+        ww, mm, vv = ref.step32(g[o:o + k].float().cpu().numpy(), x, zero, zero, h, bits)
+        same(w[o:o + k], ww, f"w at {o}")
+        if bits == 32:
+            same(m[o:o + k], mm, f"m at {o}")
+            same(v[o:o + k], vv, f"v at {o}")
+        else:
+            lo, hi = ref.halves_for(k, index + o, 1, 1)
+            for name, val, r, got, sc in (("m", mm, lo, m, ms), ("v", vv, hi, v, vs)):
+                c, s = ref.encode(val, name, r)
+                same(got[o:o + k], c, f"{name} codes at {o}")
+                same(sc[o // 256:o // 256 + s.size], s, f"{name} scales at {o}")
+    out = torch.zeros((), dtype=torch.float64, device=DEV)
+    a.zs_grad_sumsq_multi(t, out)
+    want = g.view(-1)[: n // 1024 * 1024].view(1024, -1).float().square().sum(1, dtype=torch.float64).sum()
+    want = want + g[n // 1024 * 1024:].double().square().sum()
+    # squares of bf16 are exact in fp32, the sums are in double
+    assert abs(out.item() - want.item()) <= 1e-10 * want.item()

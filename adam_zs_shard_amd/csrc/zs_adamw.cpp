@@ -15,14 +15,17 @@ namespace {
 
 constexpr int64_t kMaxLen = int64_t{1} << 60;
 // A launch counts its lanes in 32 bits: 2^24 workgroups of 256 at most.
-constexpr int64_t kMaxChunks = (int64_t{1} << 24) - 1;
+constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
 
-// Elements per workgroup.
-constexpr int64_t kChunkLarge = 8192, kChunkSmall = 2048;
+// Elements per entry of the launch table, in units of one workgroup.
+constexpr int kUnitsLarge = 3, kUnitsSmall = 0;
+constexpr int64_t kChunkLarge = int64_t{zs::kUnit} << kUnitsLarge;
+constexpr int64_t kChunkSmall = int64_t{zs::kUnit} << kUnitsSmall;
 
 int64_t chunk_rule(int64_t total) {
   return total >= 512 * kChunkLarge ? kChunkLarge : kChunkSmall;
 }
+int units_of(int64_t chunk) { return chunk == kChunkLarge ? kUnitsLarge : kUnitsSmall; }
 
 struct Layout {
   size_t chunks, gptrs, partial, total;
@@ -41,7 +44,7 @@ bool plan(int32_t npieces, int32_t p, Len len, int64_t* chunk, int64_t* nchunks,
   *chunk = chunk_rule(total);
   *nchunks = 0;
   for (int32_t i = 0; i < npieces; ++i) *nchunks += (len(i) - 1) / *chunk + 1;
-  if (*nchunks > kMaxChunks) return false;
+  if (*nchunks > kMaxGroups >> units_of(*chunk)) return false;
   out->chunks = 0;
   out->gptrs = up256(sizeof(zs::AwChunk) * static_cast<size_t>(*nchunks));
   out->partial =
@@ -126,30 +129,34 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
 
   std::vector<unsigned char> host(lay.partial, 0);
   auto* chunks = reinterpret_cast<zs::AwChunk*>(host.data() + lay.chunks);
-  auto* gptrs = reinterpret_cast<const void**>(host.data() + lay.gptrs);
+  auto* gptrs = reinterpret_cast<uint64_t*>(host.data() + lay.gptrs);
+  const auto at = [](const void* p, uintptr_t size, int64_t n) {
+    return p ? reinterpret_cast<uintptr_t>(p) + size * static_cast<uintptr_t>(n) : 0;
+  };
   int64_t c = 0;
   for (int32_t i = 0; i < npieces; ++i) {
     const zs_adamw_piece& q = pieces[i];
-    for (int32_t r = 0; r < p; ++r) gptrs[static_cast<int64_t>(i) * p + r] = q.grads[r];
-    for (int64_t at = 0; at < q.len; at += chunk) {
+    for (int32_t r = 0; r < p; ++r)
+      gptrs[static_cast<int64_t>(i) * p + r] = at(q.grads[r], gsize, 0);
+    for (int64_t e = 0; e < q.len; e += chunk) {
       zs::AwChunk& d = chunks[c++];
       if (state_bits != 0) {
-        d.w = q.w + at;
-        d.m = static_cast<char*>(q.m) + at * static_cast<int64_t>(ssize);
-        d.v = static_cast<char*>(q.v) + at * static_cast<int64_t>(ssize);
+        d.w = at(q.w, 4, e);
+        d.m = at(q.m, ssize, e);
+        d.v = at(q.v, ssize, e);
         if (state_bits == 8) {
-          d.m_scale = q.m_scale + at / ZS_STATE8_BLOCK;
-          d.v_scale = q.v_scale + at / ZS_STATE8_BLOCK;
+          d.m_scale = at(q.m_scale, 4, e / ZS_STATE8_BLOCK);
+          d.v_scale = at(q.v_scale, 4, e / ZS_STATE8_BLOCK);
         }
-        if (param_dtype != 0) d.param = static_cast<uint16_t*>(q.param) + at;
+        if (param_dtype != 0) d.param = at(q.param, 2, e);
         d.lr_scale = q.lr_scale;
         d.decay = q.weight_decay;
       }
-      d.g = static_cast<const char*>(q.grads[0]) + at * static_cast<int64_t>(gsize);
-      if (q.g_mean) d.g_mean = q.g_mean + at;
-      d.index = q.index + at;
-      d.start = at;
-      d.len = static_cast<int32_t>(std::min(chunk, q.len - at));
+      d.g = at(q.grads[0], gsize, e);
+      d.g_mean = at(q.g_mean, 4, e);
+      d.index = q.index + e;
+      d.start = e;
+      d.len = static_cast<int32_t>(std::min(chunk, q.len - e));
       d.piece = i;
     }
   }
@@ -175,7 +182,8 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
 zs_status check_table(const zs_adamw_table* t) {
   if (!t || !t->workspace) return ZS_ERR_NULL;
   if (t->p < 1 || t->p > ZS_MAX_P || t->npieces < 0 || t->nchunks < t->npieces ||
-      t->nchunks > kMaxChunks || (t->chunk_elems != kChunkLarge && t->chunk_elems != kChunkSmall) ||
+      (t->chunk_elems != kChunkLarge && t->chunk_elems != kChunkSmall) ||
+      t->nchunks > kMaxGroups >> units_of(t->chunk_elems) ||
       (t->state_bits != 0 && t->state_bits != 8 && t->state_bits != 32))
     return ZS_ERR_ARG;
   if (!grad_dtype_ok(t->grad_dtype) || !param_dtype_ok(t->param_dtype)) return ZS_ERR_DTYPE;
@@ -234,7 +242,7 @@ zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_hparams* hp, const 
   auto* base = static_cast<unsigned char*>(t->workspace);
   zs::AwLaunch L;
   L.a.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
-  L.a.gptrs = reinterpret_cast<const void* const*>(base + lay.gptrs);
+  L.a.gptrs = reinterpret_cast<const uint64_t*>(base + lay.gptrs);
   L.a.sumsq = sumsq;
   L.a.grad_scale = hp->grad_scale;
   L.a.max_norm = hp->max_norm;
@@ -242,6 +250,7 @@ zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_hparams* hp, const 
   L.a.p = t->p;
   L.a.skip_nonfinite = hp->skip_nonfinite;
   L.a.c = make_consts(*hp, t->p, t->state_bits);
+  L.a.units = units_of(t->chunk_elems);
   L.nchunks = t->nchunks;
   L.gdt = t->grad_dtype;
   L.pdt = t->param_dtype ? t->param_dtype : ZS_BF16;
@@ -310,7 +319,7 @@ zs_status zs_grad_sumsq_multi(const zs_adamw_table* t, int32_t store_mean, int32
     auto* base = static_cast<unsigned char*>(t->workspace);
     zs::SumsqLaunch L;
     L.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
-    L.gptrs = reinterpret_cast<const void* const*>(base + lay.gptrs);
+    L.gptrs = reinterpret_cast<const uint64_t*>(base + lay.gptrs);
     L.nchunks = t->nchunks;
     L.p = t->p;
     L.gdt = t->grad_dtype;

@@ -9,19 +9,18 @@ namespace zs {
 constexpr int kF32 = ZS_F32;
 constexpr int kStateBlock = ZS_STATE8_BLOCK;  // one wave: 64 lanes x 4 elements
 
-// One workgroup's share of one tensor, with every address at its first
-// element, so that a wave knows all it needs after one scalar load.
+// A run of at most chunk_elems elements of one tensor, with every address at
+// its first element, so that a wave knows all it needs after one scalar load.
+// Its workgroups take kUnit elements each.
+constexpr int kUnit = 4 * kStateBlock;
 struct AwChunk {
-  float* w;
-  void* m;
-  void* v;
-  float* m_scale;
-  float* v_scale;
-  uint16_t* param;
-  const void* g;      // rank 0's gradient
-  float* g_mean;
-  int64_t index;      // of element 0, for the random bits
-  int64_t start;      // of element 0 in its tensor
+  uint64_t w, m, v;           // addresses as numbers, see ld_chunk
+  uint64_t m_scale, v_scale;
+  uint64_t param;
+  uint64_t g;                 // rank 0's gradient
+  uint64_t g_mean;
+  int64_t index;              // of element 0, for the random bits
+  int64_t start;              // of element 0 in its tensor
   double lr_scale;
   double decay;
   int32_t len;
@@ -41,12 +40,13 @@ struct AwConsts {
 
 struct AwArgs {
   const AwChunk* chunks;
-  const void* const* gptrs;  // npieces * p rank pointers at the tensors' first elements
+  const uint64_t* gptrs;     // npieces * p rank pointers at the tensors' first elements
   const double* sumsq;       // or null
   double grad_scale, max_norm;
   uint64_t seed;
   int32_t p;
   int32_t skip_nonfinite;
+  int32_t units;  // per chunk, a power of two's exponent
   AwConsts c;
 };
 
@@ -59,7 +59,7 @@ struct AwLaunch {
 
 struct SumsqLaunch {
   const AwChunk* chunks;
-  const void* const* gptrs;
+  const uint64_t* gptrs;
   int64_t nchunks;
   int p, gdt;
   bool store, accumulate;

@@ -25,6 +25,36 @@ constexpr int kWaves = kBlock / kWave;
 // Codes may sit at any byte address.
 typedef uint32_t u32b __attribute__((aligned(1)));
 
+// An address out of a table, as one in global memory: the compiler cannot
+// know that of a pointer that it loads, and accesses through a generic one
+// (flat) make every wait a full drain.
+template <class T>
+__device__ __forceinline__ T* in_global(uint64_t x) {
+  using GT = __attribute__((address_space(1))) T;
+  return (T*)reinterpret_cast<GT*>(x);
+}
+struct Chunk {
+  float* w;
+  char* m;
+  char* v;
+  float* m_scale;
+  float* v_scale;
+  uint16_t* param;
+  const char* g;
+  float* g_mean;
+  int64_t index, start;
+  double lr_scale, decay;
+  int32_t len, piece;
+};
+__device__ __forceinline__ Chunk ld_chunk(const AwChunk* at) {
+  const AwChunk& c = *at;
+  return Chunk{in_global<float>(c.w),        in_global<char>(c.m),
+               in_global<char>(c.v),         in_global<float>(c.m_scale),
+               in_global<float>(c.v_scale),  in_global<uint16_t>(c.param),
+               in_global<const char>(c.g),   in_global<float>(c.g_mean),
+               c.index, c.start, c.lr_scale, c.decay, c.len, c.piece};
+}
+
 template <class F>
 void with_gdt(int dt, F&& f) {
   if (dt == kF16) f(IC<kF16>{});
@@ -133,7 +163,10 @@ __device__ __forceinline__ void st_codes(void* base, uint32_t lane, int n, uint3
 }
 
 // ---- gradients ----------------------------------------------------------------
-typedef const void* const __attribute__((address_space(4)))* RankPtrs;
+typedef const uint64_t __attribute__((address_space(4)))* RankPtrs;
+__device__ __forceinline__ RankPtrs rank_ptrs(const uint64_t* gptrs, int piece, int p) {
+  return (RankPtrs)(reinterpret_cast<uintptr_t>(gptrs + static_cast<int64_t>(piece) * p));
+}
 
 // Loads of R ranks for U blocks in flight together, then the adds in rank
 // order.  n < 0: whole blocks.
@@ -143,7 +176,7 @@ __device__ __forceinline__ void add_ranks(RankPtrs ptrs, int r0, int64_t byte0, 
   Raw4<GDT> q[R][U];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const char* base = static_cast<const char*>(ptrs[r0 + r]) + byte0;
+    const char* base = in_global<const char>(ptrs[r0 + r]) + byte0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const char* b = base + u * (kStateBlock * kSize<GDT>);

@@ -23,7 +23,7 @@ __device__ __forceinline__ double block_sum(double x) {
 }
 
 template <int U, int GDT, bool STORE, bool ONE>
-__device__ __forceinline__ void sumsq_blocks(const AwChunk& ch, const void* const* gptrs, int p,
+__device__ __forceinline__ void sumsq_blocks(const Chunk& ch, const uint64_t* gptrs, int p,
                                              float PF, int b, uint32_t lane, int n, double& acc) {
   const int64_t e0 = static_cast<int64_t>(b) * kStateBlock;
   float g[U][kQuad];
@@ -31,15 +31,13 @@ __device__ __forceinline__ void sumsq_blocks(const AwChunk& ch, const void* cons
     Raw4<GDT> q[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const char* gb = static_cast<const char*>(ch.g) + (e0 + u * kStateBlock) * kSize<GDT>;
+      const char* gb = ch.g + (e0 + u * kStateBlock) * kSize<GDT>;
       q[u] = n < 0 ? ld_raw4<GDT>(gb, lane) : ld_raw4<GDT>(gb, lane, n);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) widen4<GDT>(q[u], g[u]);
   } else {
-    mean_ranks<U, GDT>(
-        (RankPtrs)(reinterpret_cast<uintptr_t>(gptrs + static_cast<int64_t>(ch.piece) * p)), p, PF,
-        ch.start + e0, lane, n, g);
+    mean_ranks<U, GDT>(rank_ptrs(gptrs, ch.piece, p), p, PF, ch.start + e0, lane, n, g);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -58,14 +56,14 @@ __device__ __forceinline__ void sumsq_blocks(const AwChunk& ch, const void* cons
 
 template <int GDT, bool STORE, bool ONE>
 __global__ __launch_bounds__(kBlock) void sumsq_kernel(const AwChunk* chunks,
-                                                       const void* const* gptrs, int64_t nchunks,
+                                                       const uint64_t* gptrs, int64_t nchunks,
                                                        int p, float PF, double* partial) {
   constexpr int U = 4;
   const uint32_t lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   double acc = 0.0;
   for (int64_t c = blockIdx.x; c < nchunks; c += gridDim.x) {
-    const AwChunk ch = chunks[c];
+    const Chunk ch = ld_chunk(chunks + c);
     const int full = ch.len / kStateBlock;
     const int blocks = (ch.len + kStateBlock - 1) / kStateBlock;
     for (int b = wave * U; b < blocks; b += kWaves * U) {

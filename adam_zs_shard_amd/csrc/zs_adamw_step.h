@@ -13,7 +13,7 @@ namespace {
 // whole blocks; else (U = 1) the lane's n (0..4) elements of a tensor's last
 // block.
 template <int U, int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
-__device__ __forceinline__ void step_blocks(const AwArgs& a, const AwChunk& ch, float GS, float LR,
+__device__ __forceinline__ void step_blocks(const AwArgs& a, const Chunk& ch, float GS, float LR,
                                             float LD, int b, uint32_t lane, int n) {
   const int64_t e0 = static_cast<int64_t>(b) * kStateBlock;
   float g[U][kQuad], w[U][kQuad], m[U][kQuad], v[U][kQuad];
@@ -25,20 +25,18 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const AwChunk& ch, 
   for (int u = 0; u < U; ++u) {
     const int64_t e = e0 + u * kStateBlock;
     if constexpr (ONE) {
-      const char* gb = static_cast<const char*>(ch.g) + e * kSize<GDT>;
+      const char* gb = ch.g + e * kSize<GDT>;
       gq[u] = n < 0 ? ld_raw4<GDT>(gb, lane) : ld_raw4<GDT>(gb, lane, n);
     }
     wq[u] = n < 0 ? ld_raw4<kF32>(ch.w + e, lane) : ld_raw4<kF32>(ch.w + e, lane, n);
     if constexpr (BITS == 32) {
-      const float* mb = static_cast<const float*>(ch.m) + e;
-      const float* vb = static_cast<const float*>(ch.v) + e;
+      const float* mb = reinterpret_cast<const float*>(ch.m) + e;
+      const float* vb = reinterpret_cast<const float*>(ch.v) + e;
       mq[u] = n < 0 ? ld_raw4<kF32>(mb, lane) : ld_raw4<kF32>(mb, lane, n);
       vq[u] = n < 0 ? ld_raw4<kF32>(vb, lane) : ld_raw4<kF32>(vb, lane, n);
     } else {
-      const uint8_t* mb = static_cast<const uint8_t*>(ch.m) + e;
-      const uint8_t* vb = static_cast<const uint8_t*>(ch.v) + e;
-      mc[u] = n < 0 ? ld_codes(mb, lane) : ld_codes(mb, lane, n);
-      vc[u] = n < 0 ? ld_codes(vb, lane) : ld_codes(vb, lane, n);
+      mc[u] = n < 0 ? ld_codes(ch.m + e, lane) : ld_codes(ch.m + e, lane, n);
+      vc[u] = n < 0 ? ld_codes(ch.v + e, lane) : ld_codes(ch.v + e, lane, n);
       ms[u] = ch.m_scale[b + u];
       vs[u] = ch.v_scale[b + u];
     }
@@ -47,9 +45,7 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const AwChunk& ch, 
 #pragma unroll
     for (int u = 0; u < U; ++u) widen4<GDT>(gq[u], g[u]);
   } else {
-    mean_ranks<U, GDT>((RankPtrs)(reinterpret_cast<uintptr_t>(
-                           a.gptrs + static_cast<int64_t>(ch.piece) * a.p)),
-                       a.p, a.c.PF, ch.start + e0, lane, n, g);
+    mean_ranks<U, GDT>(rank_ptrs(a.gptrs, ch.piece, a.p), a.p, a.c.PF, ch.start + e0, lane, n, g);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -80,8 +76,8 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const AwChunk& ch, 
       if (ch.param) st_quad16<PDT>(ch.param + e, lane, n, w[u]);
     }
     if constexpr (BITS == 32) {
-      float* mb = static_cast<float*>(ch.m) + e;
-      float* vb = static_cast<float*>(ch.v) + e;
+      float* mb = reinterpret_cast<float*>(ch.m) + e;
+      float* vb = reinterpret_cast<float*>(ch.v) + e;
       if (n < 0) {
         st_quad32(mb, lane, m[u]);
         st_quad32(vb, lane, v[u]);
@@ -110,14 +106,12 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const AwChunk& ch, 
       }
       const uint32_t cm = encode4<ZS_STATE8_M, RANDOM>(m[u], sm, lo);
       const uint32_t cv = encode4<ZS_STATE8_V, RANDOM>(v[u], sv, hi);
-      uint8_t* mb = static_cast<uint8_t*>(ch.m) + e;
-      uint8_t* vb = static_cast<uint8_t*>(ch.v) + e;
       if (n < 0) {
-        st_codes(mb, lane, cm);
-        st_codes(vb, lane, cv);
+        st_codes(ch.m + e, lane, cm);
+        st_codes(ch.v + e, lane, cv);
       } else {
-        st_codes(mb, lane, n, cm);
-        st_codes(vb, lane, n, cv);
+        st_codes(ch.m + e, lane, n, cm);
+        st_codes(ch.v + e, lane, n, cv);
       }
       if (lane == 0) {
         ch.m_scale[b + u] = sm.scale;
@@ -127,29 +121,28 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const AwChunk& ch, 
   }
 }
 
-// One workgroup per chunk, its blocks dealt to its four waves in runs of U.
+// One workgroup per kUnit elements, one block per wave.  The grid sweeps the
+// tensors in order, so what is in flight at any moment is a narrow window of
+// each array: 1.0e9 elements with 32-bit moments take 4.96 ms this way, 5.12
+// with 2048 elements per workgroup, 5.35 with 8192.
 template <int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
 __global__ __launch_bounds__(kBlock) void adamw_kernel(AwArgs a) {
-  constexpr int U = 2;
-  const AwChunk ch = a.chunks[blockIdx.x];
+  const Chunk ch = ld_chunk(a.chunks + (blockIdx.x >> a.units));
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int b = static_cast<int>(blockIdx.x & ((1u << a.units) - 1u)) * kWaves + wave;
+  const int left = ch.len - b * kStateBlock;
+  if (left <= 0) return;
   const Scalars s = scalars(a);
   if (s.skip) return;
   const double lr = a.c.lr * ch.lr_scale;
   const float LR = static_cast<float>(lr), LD = static_cast<float>(lr * ch.decay);
   const uint32_t lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int full = ch.len / kStateBlock;
-  const int blocks = (ch.len + kStateBlock - 1) / kStateBlock;
-  for (int b = wave * U; b < blocks; b += kWaves * U) {
-    if (b + U <= full) {
-      step_blocks<U, GDT, PDT, BITS, RANDOM, ONE>(a, ch, s.GS, LR, LD, b, lane, -1);
-    } else {
-      for (int k = b; k < b + U && k < blocks; ++k) {
-        int n = ch.len - k * kStateBlock - kQuad * static_cast<int>(lane);
-        n = n < 0 ? 0 : n > kQuad ? kQuad : n;
-        step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, ch, s.GS, LR, LD, k, lane, n);
-      }
-    }
+  if (left >= kStateBlock) {
+    step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, ch, s.GS, LR, LD, b, lane, -1);
+  } else {
+    int n = left - kQuad * static_cast<int>(lane);
+    n = n < 0 ? 0 : n > kQuad ? kQuad : n;
+    step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, ch, s.GS, LR, LD, b, lane, n);
   }
 }
 
@@ -158,7 +151,7 @@ void launch_step(const AwLaunch& L) {
   with_gdt(L.gdt, [&](auto G) {
     with_dt(L.pdt, [&](auto H) {
       constexpr int GDT = decltype(G)::value, PDT = decltype(H)::value;
-      const dim3 grid(static_cast<unsigned>(L.nchunks)), block(kBlock);
+      const dim3 grid(static_cast<unsigned>(L.nchunks << L.a.units)), block(kBlock);
       if (L.a.p == 1)
         adamw_kernel<GDT, PDT, BITS, RANDOM, true><<<grid, block, 0, L.stream>>>(L.a);
       else

@@ -32,7 +32,6 @@ def test_workspace_bytes():
     need = a.zs_adamw_workspace_bytes
     assert need([], 1) > 0
     assert need([1], 1) >= 128 + 8
-    # one entry of 128 bytes per 2048 elements at most, one pointer per rank and tensor
     assert need([5000, 7], 8) - need([5000, 7], 1) >= 0
     assert need([2048 * 100], 1) >= 100 * 128
     assert need([10**9], 1) < 10**9 // 8192 * 128 + 4096 * 16
@@ -109,7 +108,7 @@ def test_upload_refuses_arguments():
 
 
 def _table(**over):
-    t = a.zs_adamw_table(WS, 4, 2048, 2, 2, z.ZS_BF16, z.ZS_BF16, 32, 1)
+    t = a.zs_adamw_table(WS, 4, 8192, 2, 2, z.ZS_BF16, z.ZS_BF16, 32, 1)
     for k, x in over.items():
         setattr(t, k, x)
     return t

@@ -198,6 +198,11 @@ def _stream(stream):
     if stream is None:
         import torch
 
+        # the current stream's handle without a Stream object around it: 0.3
+        # instead of 3.5 us, of the 8 us that a call took
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and torch.cuda.is_initialized():
+            return raw(torch.cuda.current_device())
         if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None

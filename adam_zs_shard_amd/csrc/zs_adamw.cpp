@@ -27,13 +27,26 @@ int64_t chunk_rule(int64_t total) {
 }
 int units_of(int64_t chunk) { return chunk == kChunkLarge ? kUnitsLarge : kUnitsSmall; }
 
+// Where the workspace's parts lie: the entries, the rank pointers, the norm's
+// count of arrivals and its partial sums (which alone are not uploaded).
 struct Layout {
-  size_t chunks, gptrs, partial, total;
+  size_t chunks, gptrs, arrived, partial, total;
 };
 
 size_t up256(size_t x) { return (x + 255u) & ~static_cast<size_t>(255u); }
 
-// Workgroups' entries, rank pointers, partial sums; false if too large.
+Layout layout(int64_t nchunks, int32_t npieces, int32_t p) {
+  Layout l;
+  l.chunks = 0;
+  l.gptrs = up256(sizeof(zs::AwChunk) * static_cast<size_t>(nchunks));
+  l.arrived = l.gptrs + up256(sizeof(void*) * static_cast<size_t>(npieces) *
+                              static_cast<size_t>(p));
+  l.partial = l.arrived + 256;
+  l.total = l.partial + up256(sizeof(double) * zs::kSumsqBlocks);
+  return l;
+}
+
+// The chunks of a list of tensors; false if it is too large for a launch.
 template <class Len>
 bool plan(int32_t npieces, int32_t p, Len len, int64_t* chunk, int64_t* nchunks, Layout* out) {
   int64_t total = 0;
@@ -45,11 +58,7 @@ bool plan(int32_t npieces, int32_t p, Len len, int64_t* chunk, int64_t* nchunks,
   *nchunks = 0;
   for (int32_t i = 0; i < npieces; ++i) *nchunks += (len(i) - 1) / *chunk + 1;
   if (*nchunks > kMaxGroups >> units_of(*chunk)) return false;
-  out->chunks = 0;
-  out->gptrs = up256(sizeof(zs::AwChunk) * static_cast<size_t>(*nchunks));
-  out->partial =
-      out->gptrs + up256(sizeof(void*) * static_cast<size_t>(npieces) * static_cast<size_t>(p));
-  out->total = out->partial + up256(sizeof(double) * zs::kSumsqBlocks);
+  *out = layout(*nchunks, npieces, p);
   return true;
 }
 
@@ -161,12 +170,10 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
     }
   }
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (!host.empty()) {
-    hipError_t e = hipMemcpyAsync(workspace, host.data(), host.size(), hipMemcpyHostToDevice, s);
-    if (e != hipSuccess) return static_cast<zs_status>(zs::hip_status(e));
-    e = hipStreamSynchronize(s);
-    if (e != hipSuccess) return static_cast<zs_status>(zs::hip_status(e));
-  }
+  hipError_t e = hipMemcpyAsync(workspace, host.data(), host.size(), hipMemcpyHostToDevice, s);
+  if (e != hipSuccess) return static_cast<zs_status>(zs::hip_status(e));
+  e = hipStreamSynchronize(s);
+  if (e != hipSuccess) return static_cast<zs_status>(zs::hip_status(e));
   table->workspace = workspace;
   table->nchunks = nchunks;
   table->chunk_elems = chunk;
@@ -210,24 +217,14 @@ zs::AwConsts make_consts(const zs_adamw_hparams& h, int32_t p, int32_t bits) {
   c.C1 = static_cast<float>(1.0 - h.beta1);
   c.B2 = static_cast<float>(h.beta2);
   c.C2 = static_cast<float>(1.0 - h.beta2);
-  c.A1 = static_cast<float>(bits == 32 ? bc1 : 1.0 / bc1);
+  c.A1 = static_cast<float>(bc1);
   c.A2 = static_cast<float>(bits == 32 ? bc2 : 1.0 / std::sqrt(bc2));
   c.EPS = static_cast<float>(h.eps);
   c.PF = static_cast<float>(static_cast<double>(p));
   c.lr = h.lr;
+  c.inv_bc1 = 1.0 / bc1;
   c.step = h.step;
   return c;
-}
-
-// Where the workspace's parts lie: the table's own sizes decide.
-Layout layout_of(const zs_adamw_table& t) {
-  Layout l;
-  l.chunks = 0;
-  l.gptrs = up256(sizeof(zs::AwChunk) * static_cast<size_t>(t.nchunks));
-  l.partial = l.gptrs + up256(sizeof(void*) * static_cast<size_t>(t.npieces) *
-                              static_cast<size_t>(t.p));
-  l.total = l.partial + up256(sizeof(double) * zs::kSumsqBlocks);
-  return l;
 }
 
 zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_hparams* hp, const double* sumsq,
@@ -238,7 +235,7 @@ zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_hparams* hp, const 
   if (!sumsq && (hp->max_norm > 0.0 || hp->skip_nonfinite)) return ZS_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(sumsq) % sizeof(double) != 0) return ZS_ERR_ARG;
   if (t->nchunks == 0) return ZS_OK;
-  const Layout lay = layout_of(*t);
+  const Layout lay = layout(t->nchunks, t->npieces, t->p);
   auto* base = static_cast<unsigned char*>(t->workspace);
   zs::AwLaunch L;
   L.a.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
@@ -315,7 +312,7 @@ zs_status zs_grad_sumsq_multi(const zs_adamw_table* t, int32_t store_mean, int32
         reinterpret_cast<uintptr_t>(sumsq) % sizeof(double) != 0)
       return ZS_ERR_ARG;
     if (store_mean && t->npieces > 0 && !t->has_mean) return ZS_ERR_NULL;
-    const Layout lay = layout_of(*t);
+    const Layout lay = layout(t->nchunks, t->npieces, t->p);
     auto* base = static_cast<unsigned char*>(t->workspace);
     zs::SumsqLaunch L;
     L.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
@@ -326,6 +323,7 @@ zs_status zs_grad_sumsq_multi(const zs_adamw_table* t, int32_t store_mean, int32
     L.store = store_mean != 0;
     L.accumulate = accumulate != 0;
     L.partial = reinterpret_cast<double*>(base + lay.partial);
+    L.arrived = reinterpret_cast<unsigned int*>(base + lay.arrived);
     L.out = sumsq;
     L.stream = static_cast<hipStream_t>(stream);
     const hipError_t e = zs::launch_sumsq(L);

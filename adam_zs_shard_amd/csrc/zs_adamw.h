@@ -32,9 +32,10 @@ static_assert(sizeof(AwChunk) == 128, "one table entry per 128-byte line");
 // The scalars of one step, each computed in double and rounded once.
 struct AwConsts {
   float B1, C1, B2, C2;
-  float A1, A2;  // 32-bit states: 1-beta1^t, 1-beta2^t; 8-bit: f32(1/(1-beta1^t)), f32(1/sqrt(1-beta2^t))
+  float A1, A2;  // 32-bit states: 1-beta1^t, 1-beta2^t; 8-bit: A2 = 1/sqrt(1-beta2^t)
   float EPS, PF;
   double lr;
+  double inv_bc1;  // 8-bit states: 1/(1-beta1^t)
   int64_t step;
 };
 
@@ -63,7 +64,8 @@ struct SumsqLaunch {
   int64_t nchunks;
   int p, gdt;
   bool store, accumulate;
-  double* partial;  // kSumsqBlocks doubles
+  double* partial;         // kSumsqBlocks doubles
+  unsigned int* arrived;   // 0 between launches
   double* out;
   hipStream_t stream;
 };

@@ -200,7 +200,11 @@ __device__ __forceinline__ void mean_ranks(RankPtrs ptrs, int p, float PF, int64
                                            uint32_t lane, int n, float (&s)[U][kQuad]) {
   const int64_t byte0 = at * kSize<GDT>;
   int r = 0;
-  for (; r + 4 <= p; r += 4) add_ranks<4, U, GDT>(ptrs, r, byte0, lane, n, s);
+  for (; r + 8 <= p; r += 8) add_ranks<8, U, GDT>(ptrs, r, byte0, lane, n, s);
+  if (r + 4 <= p) {
+    add_ranks<4, U, GDT>(ptrs, r, byte0, lane, n, s);
+    r += 4;
+  }
   if (r + 2 <= p) {
     add_ranks<2, U, GDT>(ptrs, r, byte0, lane, n, s);
     r += 2;
@@ -241,50 +245,50 @@ __device__ __forceinline__ uint32_t mag_bits(float x) {
   return __float_as_uint(x) & 0x7fffffffu;
 }
 
+template <int KIND>
+constexpr float kTop = KIND == ZS_STATE8_M ? kTopM : kTopV;
+template <int KIND>  // the smallest normal code
+constexpr float kLeast = KIND == ZS_STATE8_M ? 0x1p-6f : 0x1p-14f;
+
+// One over the type's largest value, rounded once.
+template <int KIND>
+constexpr float kDown = static_cast<float>(1.0 / static_cast<double>(kTop<KIND>));
+
+// A block's largest value, of its magnitudes' bits: what becomes of it.
 struct BlockScale {
   float scale;    // stored
   float inverse;  // the values' factor before they are rounded
+  bool codes;     // neither a block of zeros nor one that is not finite
 };
 
 template <int KIND>
 __device__ __forceinline__ BlockScale block_scale(uint32_t most) {
-  constexpr float top = KIND == ZS_STATE8_M ? kTopM : kTopV;
-  constexpr float down = static_cast<float>(1.0 / static_cast<double>(top));
-  BlockScale s{0.0f, 0.0f};
+  BlockScale s{0.0f, 0.0f, most >= kTinyBits && most < kInfBits};
   if (most >= kTinyBits) {
-    s.scale = __uint_as_float(most) * down;
-    s.inverse = top / __uint_as_float(most);
+    s.scale = __uint_as_float(most) * kDown<KIND>;
+    s.inverse = kTop<KIND> / __uint_as_float(most);
   }
   if (most >= kInfBits) s.scale = __uint_as_float(0x7fc00000u);
   return s;
 }
 
-// Random rounding: y's magnitude on the grid of its type, up with the
-// probability that its place between two neighbours says (16 bits of it).
-template <int KIND>
-__device__ __forceinline__ float to_grid(float y, uint32_t half) {
-  constexpr int kCut = KIND == ZS_STATE8_M ? 20 : 21;
-  constexpr float kLeast = KIND == ZS_STATE8_M ? 0x1p-6f : 0x1p-14f;
-  const float mag = __builtin_fabsf(y);
-  const bool low = mag < kLeast;  // the even part of the grid
-  const float up = low ? mag + kLeast : mag;
-  const uint32_t r = (half << (kCut - 16)) + (1u << (kCut - 17));
-  const float cut = __uint_as_float((__float_as_uint(up) + r) & ~((1u << kCut) - 1u));
-  return __builtin_copysignf(low ? cut - kLeast : cut, y);
+// Both moments' scales with one division: lanes 0..31 work on m, the others
+// on v.  `mine` is the lane's half's stored scale.
+__device__ __forceinline__ void block_scales(uint32_t mm, uint32_t vm, uint32_t lane,
+                                             BlockScale& sm, BlockScale& sv, float& mine) {
+  const bool hi = lane >= kWave / 2;
+  const uint32_t most = hi ? vm : mm;
+  const float inverse = (hi ? kTopV : kTopM) / __uint_as_float(most);
+  const float scale = __uint_as_float(most) * (hi ? kDown<ZS_STATE8_V> : kDown<ZS_STATE8_M>);
+  mine = most >= kInfBits ? __uint_as_float(0x7fc00000u) : most >= kTinyBits ? scale : 0.0f;
+  sm.inverse = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inverse), 0));
+  sv.inverse = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inverse), kWave / 2));
+  sm.codes = mm >= kTinyBits && mm < kInfBits;
+  sv.codes = vm >= kTinyBits && vm < kInfBits;
 }
 
-// Four values to codes: x * inverse cut to [-top, top], to the nearest code
-// (or to_grid's), a positive v never to code 0.
-template <int KIND, bool RANDOM>
-__device__ __forceinline__ uint32_t encode4(const float (&x)[kQuad], const BlockScale& s,
-                                            const uint32_t (&half)[kQuad]) {
-  constexpr float top = KIND == ZS_STATE8_M ? kTopM : kTopV;
-  float y[kQuad];
-#pragma unroll
-  for (int j = 0; j < kQuad; ++j) {
-    y[j] = __builtin_fminf(__builtin_fmaxf(x[j] * s.inverse, -top), top);
-    if constexpr (RANDOM) y[j] = to_grid<KIND>(y[j], half[j]);
-  }
+template <int KIND>
+__device__ __forceinline__ uint32_t pack4(const float (&y)[kQuad]) {
   int c = 0;
   if constexpr (KIND == ZS_STATE8_M) {
     c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], c, false);
@@ -293,13 +297,70 @@ __device__ __forceinline__ uint32_t encode4(const float (&x)[kQuad], const Block
     c = __builtin_amdgcn_cvt_pk_bf8_f32(y[0], y[1], c, false);
     c = __builtin_amdgcn_cvt_pk_bf8_f32(y[2], y[3], c, true);
   }
-  uint32_t u = static_cast<uint32_t>(c);
+  return static_cast<uint32_t>(c);
+}
+
+// Random rounding of a magnitude that may lie on the even part of the grid.
+template <int KIND>
+__device__ __forceinline__ float to_grid(float y, uint32_t half) {
+  constexpr int kCut = KIND == ZS_STATE8_M ? 20 : 21;
+  const float mag = __builtin_fabsf(y);
+  const bool low = mag < kLeast<KIND>;
+  const float up = low ? mag + kLeast<KIND> : mag;
+  const uint32_t r = (half << (kCut - 16)) + (1u << (kCut - 17));
+  const float cut = __uint_as_float((__float_as_uint(up) + r) & ~((1u << kCut) - 1u));
+  return __builtin_copysignf(low ? cut - kLeast<KIND> : cut, y);
+}
+
+// Four values to codes: x * inverse cut to [-top, top], to the nearest code or
+// by the random halves (m: the words' low 16 bits, v: the high ones), a
+// positive v never to code 0.  Every lane must be active.  The hardware's
+// random rounding (v_cvt_sr) adds its bits to a normal value's fraction and
+// cuts, which is the definition with the half above and a single bit below
+// it; values on the even part of the grid, and v's that might get code 0, are
+// rare, and a wave that has one takes the longer way.
+template <int KIND, bool RANDOM>
+__device__ __forceinline__ uint32_t encode4(const float (&x)[kQuad], const BlockScale& s,
+                                            const uint32_t (&word)[kQuad]) {
+  if (!s.codes) return 0u;
+  constexpr float top = kTop<KIND>;
+  float y[kQuad];
+#pragma unroll
+  for (int j = 0; j < kQuad; ++j)
+    y[j] = __builtin_fminf(__builtin_fmaxf(x[j] * s.inverse, -top), top);
+  if constexpr (!RANDOM && KIND == ZS_STATE8_M) return pack4<KIND>(y);
+  const float least =
+      __builtin_fminf(__builtin_fminf(__builtin_fabsf(y[0]), __builtin_fabsf(y[1])),
+                      __builtin_fminf(__builtin_fabsf(y[2]), __builtin_fabsf(y[3])));
+  const bool special = __builtin_amdgcn_ballot_w64(least < kLeast<KIND>) != 0;
+  if (!special) {
+    if constexpr (!RANDOM) return pack4<KIND>(y);
+    int c = 0;
+    if constexpr (KIND == ZS_STATE8_M) {
+      c = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], (word[0] << 16) | 0x8000u, c, 0);
+      c = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], (word[1] << 16) | 0x8000u, c, 1);
+      c = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], (word[2] << 16) | 0x8000u, c, 2);
+      c = __builtin_amdgcn_cvt_sr_fp8_f32(y[3], (word[3] << 16) | 0x8000u, c, 3);
+    } else {
+      c = __builtin_amdgcn_cvt_sr_bf8_f32(y[0], (word[0] & 0xffff0000u) | 0x8000u, c, 0);
+      c = __builtin_amdgcn_cvt_sr_bf8_f32(y[1], (word[1] & 0xffff0000u) | 0x8000u, c, 1);
+      c = __builtin_amdgcn_cvt_sr_bf8_f32(y[2], (word[2] & 0xffff0000u) | 0x8000u, c, 2);
+      c = __builtin_amdgcn_cvt_sr_bf8_f32(y[3], (word[3] & 0xffff0000u) | 0x8000u, c, 3);
+    }
+    return static_cast<uint32_t>(c);
+  }
+  if constexpr (RANDOM) {
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j)
+      y[j] = to_grid<KIND>(y[j], KIND == ZS_STATE8_M ? word[j] & 0xffffu : word[j] >> 16);
+  }
+  uint32_t u = pack4<KIND>(y);
   if constexpr (KIND == ZS_STATE8_V) {
 #pragma unroll
     for (int j = 0; j < kQuad; ++j)
       if (x[j] > 0.0f && ((u >> (8 * j)) & 0xffu) == 0u) u |= 1u << (8 * j);
   }
-  return s.scale > 0.0f ? u : 0u;  // no codes for a block of zeros or a NaN scale
+  return u;
 }
 
 template <int KIND>
@@ -330,9 +391,9 @@ __device__ __forceinline__ void philox(uint64_t at, uint64_t step, uint64_t seed
   for (int i = 0; i < 7; ++i) {
     const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u;
     const uint64_t b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-    c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+    c0 = __builtin_amdgcn_bitop3_b32(static_cast<uint32_t>(b >> 32), c1, k0, 0x96);  // xor
     c1 = static_cast<uint32_t>(b);
-    c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+    c2 = __builtin_amdgcn_bitop3_b32(static_cast<uint32_t>(a >> 32), c3, k1, 0x96);
     c3 = static_cast<uint32_t>(a);
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;

@@ -54,10 +54,20 @@ __device__ __forceinline__ void sumsq_blocks(const Chunk& ch, const uint64_t* gp
   }
 }
 
-template <int GDT, bool STORE, bool ONE>
+// Joining the workgroups' sums.  JOIN: the last workgroup to arrive adds them
+// up, in their order whoever it is, and makes the count ready for the next
+// launch.  That saves a launch (8 -> 5 us of the host's time for 50,000
+// elements), but each arrival writes back and invalidates its L2: with 1024
+// workgroups it cost 40 us (15.6M elements, 8 ranks: 62 -> 105 us), so only
+// launches of at most kJoinMost workgroups do it; the others join in a
+// second launch.
+constexpr int kJoinMost = 64;
+template <int GDT, bool STORE, bool ONE, bool JOIN>
 __global__ __launch_bounds__(kBlock) void sumsq_kernel(const AwChunk* chunks,
                                                        const uint64_t* gptrs, int64_t nchunks,
-                                                       int p, float PF, double* partial) {
+                                                       int p, float PF, double* partial,
+                                                       unsigned int* arrived, int accumulate,
+                                                       double* out) {
   constexpr int U = 4;
   const uint32_t lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -79,8 +89,28 @@ __global__ __launch_bounds__(kBlock) void sumsq_kernel(const AwChunk* chunks,
     }
   }
   const double s = block_sum(acc);
-  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+  if constexpr (!JOIN) {
+    if (threadIdx.x == 0) partial[blockIdx.x] = s;
+  } else {
+    __shared__ bool last;
+    if (threadIdx.x == 0) {
+      __hip_atomic_store(partial + blockIdx.x, s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+             gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    acc = 0.0;
+    if (threadIdx.x < gridDim.x)
+      acc = __hip_atomic_load(partial + threadIdx.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const double total = block_sum(acc);
+    if (threadIdx.x == 0) {
+      *out = accumulate ? *out + total : total;
+      __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
 }
+static_assert(kJoinMost <= kBlock, "one sum per thread in the join");
 
 __global__ __launch_bounds__(kBlock) void sumsq_join_kernel(const double* partial, int n,
                                                             int accumulate, double* out) {
@@ -158,21 +188,27 @@ hipError_t launch_sumsq(const SumsqLaunch& L) {
   int64_t grid = static_cast<int64_t>(cu_count()) * 4;
   if (grid > kSumsqBlocks) grid = kSumsqBlocks;
   if (grid > L.nchunks) grid = L.nchunks;
+  if (grid < 1) grid = 1;  // no tensors: the sum is still written
   const float PF = static_cast<float>(static_cast<double>(L.p));
-  if (grid > 0) with_gdt(L.gdt, [&](auto G) {
+  with_gdt(L.gdt, [&](auto G) {
     constexpr int GDT = decltype(G)::value;
     const dim3 gd(static_cast<unsigned>(grid)), bd(kBlock);
-    const auto go = [&](auto store, auto one) {
-      sumsq_kernel<GDT, decltype(store)::value != 0, decltype(one)::value != 0>
-          <<<gd, bd, 0, L.stream>>>(L.chunks, L.gptrs, L.nchunks, L.p, PF, L.partial);
+    const auto go = [&](auto store, auto one, auto join) {
+      sumsq_kernel<GDT, decltype(store)::value != 0, decltype(one)::value != 0,
+                   decltype(join)::value != 0>
+          <<<gd, bd, 0, L.stream>>>(L.chunks, L.gptrs, L.nchunks, L.p, PF, L.partial, L.arrived,
+                                    L.accumulate ? 1 : 0, L.out);
+    };
+    const auto go2 = [&](auto store, auto one) {
+      grid <= kJoinMost ? go(store, one, IC<1>{}) : go(store, one, IC<0>{});
     };
     if (L.store)
-      L.p == 1 ? go(IC<1>{}, IC<1>{}) : go(IC<1>{}, IC<0>{});
+      L.p == 1 ? go2(IC<1>{}, IC<1>{}) : go2(IC<1>{}, IC<0>{});
     else
-      L.p == 1 ? go(IC<0>{}, IC<1>{}) : go(IC<0>{}, IC<0>{});
+      L.p == 1 ? go2(IC<0>{}, IC<1>{}) : go2(IC<0>{}, IC<0>{});
   });
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || grid <= kJoinMost) return e;
   sumsq_join_kernel<<<dim3(1), dim3(kBlock), 0, L.stream>>>(L.partial, static_cast<int>(grid),
                                                             L.accumulate ? 1 : 0, L.out);
   return hipGetLastError();

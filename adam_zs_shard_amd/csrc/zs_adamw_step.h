@@ -62,10 +62,15 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const Chunk& ch, fl
     for (int j = 0; j < kQuad; ++j) {
       moments1(a.c, g[u][j] * GS, m[u][j], v[u][j]);
       float x;
-      if constexpr (BITS == 32)
+      if constexpr (BITS == 32) {
         x = (m[u][j] / a.c.A1) / (__builtin_sqrtf(v[u][j] / a.c.A2) + a.c.EPS);
-      else
-        x = (m[u][j] * a.c.A1) / (__builtin_sqrtf(v[u][j]) * a.c.A2 + a.c.EPS);
+      } else {
+        // the hardware's root and reciprocal: the 8-bit step is as much bound
+        // by its arithmetic as by HBM, and moments that are held to 2^-4 need
+        // no correctly rounded quotient
+        x = m[u][j] *
+            __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[u][j]) * a.c.A2 + a.c.EPS);
+      }
       w[u][j] = w[u][j] - (LR * x + LD * w[u][j]);
     }
     if (n < 0) {
@@ -87,25 +92,22 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const Chunk& ch, fl
       }
     } else {
       // elements behind the tensor's end are zeros here: they raise no maximum
+      // (v is never negative, so its bits are its magnitude's)
       uint32_t mm = 0, vm = 0;
 #pragma unroll
       for (int j = 0; j < kQuad; ++j) {
         mm = mag_bits(m[u][j]) > mm ? mag_bits(m[u][j]) : mm;
-        vm = mag_bits(v[u][j]) > vm ? mag_bits(v[u][j]) : vm;
+        vm = __float_as_uint(v[u][j]) > vm ? __float_as_uint(v[u][j]) : vm;
       }
-      const BlockScale sm = block_scale<ZS_STATE8_M>(wave_max(mm));
-      const BlockScale sv = block_scale<ZS_STATE8_V>(wave_max(vm));
-      uint32_t r[kQuad] = {0u, 0u, 0u, 0u}, lo[kQuad], hi[kQuad];
+      BlockScale sm, sv;
+      float mine;
+      block_scales(wave_max(mm), wave_max(vm), lane, sm, sv, mine);
+      uint32_t word[kQuad] = {0u, 0u, 0u, 0u};
       if constexpr (RANDOM)
         philox(static_cast<uint64_t>(ch.index + e + kQuad * lane),
-               static_cast<uint64_t>(a.c.step), a.seed, r);
-#pragma unroll
-      for (int j = 0; j < kQuad; ++j) {
-        lo[j] = r[j] & 0xffffu;
-        hi[j] = r[j] >> 16;
-      }
-      const uint32_t cm = encode4<ZS_STATE8_M, RANDOM>(m[u], sm, lo);
-      const uint32_t cv = encode4<ZS_STATE8_V, RANDOM>(v[u], sv, hi);
+               static_cast<uint64_t>(a.c.step), a.seed, word);
+      const uint32_t cm = encode4<ZS_STATE8_M, RANDOM>(m[u], sm, word);
+      const uint32_t cv = encode4<ZS_STATE8_V, RANDOM>(v[u], sv, word);
       if (n < 0) {
         st_codes(ch.m + e, lane, cm);
         st_codes(ch.v + e, lane, cv);
@@ -113,10 +115,7 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const Chunk& ch, fl
         st_codes(ch.m + e, lane, n, cm);
         st_codes(ch.v + e, lane, n, cv);
       }
-      if (lane == 0) {
-        ch.m_scale[b + u] = sm.scale;
-        ch.v_scale[b + u] = sv.scale;
-      }
+      if (lane % (kWave / 2) == 0) (lane == 0 ? ch.m_scale : ch.v_scale)[b + u] = mine;
     }
   }
 }
@@ -135,7 +134,8 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(AwArgs a) {
   const Scalars s = scalars(a);
   if (s.skip) return;
   const double lr = a.c.lr * ch.lr_scale;
-  const float LR = static_cast<float>(lr), LD = static_cast<float>(lr * ch.decay);
+  const float LR = static_cast<float>(BITS == 32 ? lr : lr * a.c.inv_bc1);
+  const float LD = static_cast<float>(lr * ch.decay);
   const uint32_t lane = threadIdx.x % kWave;
   if (left >= kStateBlock) {
     step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, ch, s.GS, LR, LD, b, lane, -1);

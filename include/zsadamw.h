@@ -17,8 +17,10 @@
  *   param = w' rounded to nearest-even fp16/bf16
  * With 32-bit states m_hat = m'/(1-beta1^t) and v_hat = v'/(1-beta2^t): with
  * no decay, no clipping and lr_scale 1 the step is ZS_ADAM_STANDARD's, bit
- * for bit.  With 8-bit states u = (m' * f32(1/(1-beta1^t))) / (sqrt(v') *
- * f32(1/sqrt(1-beta2^t)) + eps), from the moments before they are rounded.
+ * for bit.  With 8-bit states lr_i*u is f32(lr_i/(1-beta1^t)) * (m' /
+ * (sqrt(v') * f32(1/sqrt(1-beta2^t)) + eps)), from the moments before they
+ * are rounded, where the root and the reciprocal are the hardware's, within
+ * 1 ulp each, and a v' or a divisor below 2^-126 counts as 0.
  * gs = f32(grad_scale * coef), coef = min(1, max_norm / (sqrt(sumsq) *
  * |grad_scale| + 1e-6)) in double where a norm is given, else 1.
  *

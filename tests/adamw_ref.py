@@ -40,7 +40,12 @@ def mean32(grads):
 
 def step32(g, w, m, v, h, bits=32):
     """One step of the fp32 sequence from the mean gradient; h: dict of lr (the
-    tensor's), decay, beta1, beta2, eps, step, gs.  Returns (w, m, v)."""
+    tensor's), decay, beta1, beta2, eps, step, gs.  Returns (w, m, v) and, for
+    8 bits, how far the hardware's root and reciprocal may take w from here:
+    relative to u, root 2 U (1 ulp) + U here, its constant, product and sum 3 U
+    on each side, reciprocal 2 U, product U and the folded constant U against
+    the constant, product and quotient 3 U here: under 18 U; then a product and
+    two sums on each side, U of each one's result."""
     b1, b2, t = h["beta1"], h["beta2"], h["step"]
     bc1, bc2 = 1.0 - b1 ** t, 1.0 - b2 ** t
     with np.errstate(all="ignore"):
@@ -51,11 +56,15 @@ def step32(g, w, m, v, h, bits=32):
             u = (m / F(bc1)) / (np.sqrt(v / F(bc2)) + F(h["eps"]))
         else:
             u = (m * F(1.0 / bc1)) / (np.sqrt(v) * F(1.0 / np.sqrt(bc2)) + F(h["eps"]))
-        w = w - (F(h["lr"]) * u + F(h["lr"] * h["decay"]) * w)
-    return w, m, v
+        lu, lw = F(h["lr"]) * u, F(h["lr"] * h["decay"]) * w
+        w = w - (lu + lw)
+        if bits == 32:
+            return w, m, v
+        off = U * (22.0 * np.abs(lu).astype(np.float64) + 4.0 * np.abs(lw) + 2.1 * np.abs(w))
+    return w, m, v, off
 
 
-def step64(grads, w, m, v, h):
+def step64(grads, w, m, v, h, bits=32):
     """The definition in 64 bits and bounds on the fp32 sequence's distance:
     (w, m, v, bw, bm, bv).  Each operation, constant and sum in fp32 is off by
     at most U relative (no product here underflows: the tests' values do not)."""
@@ -77,7 +86,9 @@ def step64(grads, w, m, v, h):
     # m_hat: the constant and a division; the root: half of v's relative error, the constant, two roundings,
     # the sum with eps (eps rounded too); then the quotient
     rel_d = np.divide(bv, 2 * v2, out=np.zeros_like(v2), where=v2 > 0) * (1 + 1e-3) + 5.1 * U
-    bu = bm / (1 - b1 ** t) / d + np.abs(u) * (rel_d + 3.1 * U)
+    if bits == 8:  # a root of 1 ulp (2 U), and a reciprocal of 1 ulp and a product for the quotient
+        rel_d += 1.1 * U
+    bu = bm / (1 - b1 ** t) / d + np.abs(u) * (rel_d + (3.1 if bits == 32 else 5.1) * U)
     lr, ld = h["lr"], h["lr"] * h["decay"]
     w2 = w - (lr * u + ld * w)
     bw = abs(lr) * bu + 3.2 * U * (np.abs(lr * u) + np.abs(ld * w)) + 1.1 * U * np.abs(w2)

@@ -38,8 +38,9 @@ def same(got, want, what):
         nan = np.isnan(want)
         assert np.array_equal(nan, np.isnan(got.detach().float().cpu().numpy())), what
         g, w = g[~nan], w[~nan]
-    assert g.shape == w.shape and np.array_equal(g, w), \
-        f"{what}: {int((g != w).sum())} of {w.size} differ in bits"
+    assert g.shape == w.shape, what
+    differ = int((g != w).sum())
+    assert differ == 0, f"{what}: {differ} of {w.size} differ in bits"
 
 
 class Buffers:
@@ -159,14 +160,21 @@ class Model:
         for i, (n, d) in enumerate(zip(self.lens, before)):
             h = dict(lr=LR * self.lr_scale[i], decay=self.decay[i], beta1=B1, beta2=B2, eps=EPS,
                      step=step, gs=gs)
-            w, m, v = ref.step32(ref.mean32(d["g"]), d["w"], d["m"], d["v"], h, self.bits)
+            w, m, v, *off = ref.step32(ref.mean32(d["g"]), d["w"], d["m"], d["v"], h, self.bits)
             what = f"tensor {i} of {n}"
-            same(self.w[i], w, what + " w")
+            got = self.w[i].cpu().numpy()
+            if self.bits == 32:
+                same(self.w[i], w, what + " w")
+            else:
+                fine = np.isfinite(w)
+                assert np.array_equal(fine, np.isfinite(got)), what
+                far = np.abs(got[fine] - w[fine].astype(np.float64))
+                assert np.all(far <= off[0][fine]), f"{what} w: {float((far / off[0][fine]).max())}"
             if self.pb:  # a NaN is a NaN, whatever its bits
                 fine = ~np.isnan(w)
                 assert np.array_equal(fine, ~np.isnan(self.pb[i].float().cpu().numpy()))
                 same(self.pb[i][torch.from_numpy(fine).to(DEV)],
-                     torch.from_numpy(w[fine]).to(TD[self.param]).view(torch.int16).numpy(),
+                     torch.from_numpy(got[fine]).to(TD[self.param]).view(torch.int16).numpy(),
                      what + " param")
             if self.bits == 32:
                 same(self.m[i], m, what + " m")
@@ -179,10 +187,9 @@ class Model:
                     codes, scales = ref.encode(x, k, r)
                     same(getattr(self, k)[i], codes, what + f" {k} codes")
                     same(getattr(self, k + "s")[i], scales, what + f" {k} scales")
-            if bounds and n >= 1:
-                w64, m64, v64, bw, bm, bv = ref.step64(d["g"], d["w"], d["m"], d["v"], h)
-                # the 8-bit form multiplies by rounded reciprocals where the other divides
-                assert np.all(np.abs(self.w[i].cpu().numpy() - w64) <= bw * (1 if self.bits == 32 else 1.5))
+            if bounds:
+                w64, m64, v64, bw, bm, bv = ref.step64(d["g"], d["w"], d["m"], d["v"], h, self.bits)
+                assert np.all(np.abs(got - w64) <= bw)
                 if self.bits == 32:
                     assert np.all(np.abs(self.m[i].cpu().numpy() - m64) <= bm)
                     assert np.all(np.abs(self.v[i].cpu().numpy() - v64) <= bv)
@@ -321,7 +328,7 @@ def test_stochastic_rounding_keeps_the_mean_over_steps():
     keep = [b.flat.clone() for b in M.all()]
     d = M.host(0)
     h = dict(lr=LR, decay=0.1, beta1=B1, beta2=B2, eps=EPS, step=5, gs=1.0)
-    _, m, v = ref.step32(ref.mean32(d["g"]), d["w"], d["m"], d["v"], h, 8)
+    _, m, v, _ = ref.step32(ref.mean32(d["g"]), d["w"], d["m"], d["v"], h, 8)
     sums = {"m": 0.0, "v": 0.0}
     for seed in range(seeds):
         for b, x in zip(M.all(), keep):
@@ -545,12 +552,13 @@ def test_offsets_beyond_32_bits(bits):
     h = dict(lr=LR, decay=0.1, beta1=B1, beta2=B2, eps=EPS, step=1, gs=1.0)
     for (o, k), x in zip(parts, w0):
         zero = np.zeros(k, np.float32)
-        ww, mm, vv = ref.step32(g[o:o + k].float().cpu().numpy(), x, zero, zero, h, bits)
-        same(w[o:o + k], ww, f"w at {o}")
+        ww, mm, vv, *off = ref.step32(g[o:o + k].float().cpu().numpy(), x, zero, zero, h, bits)
         if bits == 32:
+            same(w[o:o + k], ww, f"w at {o}")
             same(m[o:o + k], mm, f"m at {o}")
             same(v[o:o + k], vv, f"v at {o}")
         else:
+            assert np.all(np.abs(w[o:o + k].cpu().numpy() - ww.astype(np.float64)) <= off[0])
             lo, hi = ref.halves_for(k, index + o, 1, 1)
             for name, val, r, got, sc in (("m", mm, lo, m, ms), ("v", vv, hi, v, vs)):
                 c, s = ref.encode(val, name, r)

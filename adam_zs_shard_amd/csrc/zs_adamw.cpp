@@ -46,7 +46,19 @@ Layout layout(int64_t nchunks, int32_t npieces, int32_t p) {
   return l;
 }
 
-// The chunks of a list of tensors; false if it is too large for a launch.
+// A tensor's first chunk may be up to kHeadMost - 1 elements short, so that the
+// others begin on whole lines of memory (head_of).
+constexpr int kHeadMost = 64;
+
+// Chunks of a tensor whose first one is `head` short of a chunk or, with head
+// 0, whole.
+int64_t chunks_of(int64_t len, int64_t chunk, int head) {
+  const int64_t first = head == 0 ? chunk : chunk - kHeadMost + head;
+  return len <= first ? 1 : 1 + (len - first - 1) / chunk + 1;
+}
+
+// The most chunks that a list of tensors may come to, and the workspace for
+// them; false if they are too many for a launch.
 template <class Len>
 bool plan(int32_t npieces, int32_t p, Len len, int64_t* chunk, int64_t* nchunks, Layout* out) {
   int64_t total = 0;
@@ -56,7 +68,7 @@ bool plan(int32_t npieces, int32_t p, Len len, int64_t* chunk, int64_t* nchunks,
   }
   *chunk = chunk_rule(total);
   *nchunks = 0;
-  for (int32_t i = 0; i < npieces; ++i) *nchunks += (len(i) - 1) / *chunk + 1;
+  for (int32_t i = 0; i < npieces; ++i) *nchunks += chunks_of(len(i), *chunk, 1);
   if (*nchunks > kMaxGroups >> units_of(*chunk)) return false;
   *out = layout(*nchunks, npieces, p);
   return true;
@@ -65,6 +77,35 @@ bool plan(int32_t npieces, int32_t p, Len len, int64_t* chunk, int64_t* nchunks,
 struct Span {
   uintptr_t lo, hi;
 };
+
+// An array of a tensor: where it begins, its element size, and the bytes per
+// element that it moves.
+struct Stream {
+  uintptr_t at;
+  unsigned size, weight;
+};
+
+// The elements (0..63) before the first chunk boundary of a tensor, chosen so
+// that from there on its arrays' accesses start as near to whole 128-byte
+// lines as they can.  1.0e9 elements with 32-bit moments in buffers that begin
+// 12 bytes into a line: 5.47 ms with chunks from the first element on, 4.83
+// with this (4.79 where all begin on a line).
+int head_of(const std::vector<Stream>& streams) {
+  int best = 0, best_score = -1;
+  for (int h = 0; h < kHeadMost; ++h) {
+    int score = 0;
+    for (const Stream& s : streams) {
+      const uintptr_t a = s.at + static_cast<uintptr_t>(h) * s.size;
+      const int level = a % 128u == 0 ? 8 : a % 64u == 0 ? 6 : a % 16u == 0 ? 2 : a % 8u == 0;
+      score += level * static_cast<int>(s.weight);
+    }
+    if (score > best_score) {
+      best_score = score;
+      best = h;
+    }
+  }
+  return best;
+}
 
 bool grad_dtype_ok(int32_t dt) { return dt == ZS_F16 || dt == ZS_BF16 || dt == ZS_F32; }
 bool param_dtype_ok(int32_t dt) { return dt == 0 || dt == ZS_F16 || dt == ZS_BF16; }
@@ -136,6 +177,32 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
     if (reach > wr.lo) return ZS_ERR_ALIAS;
   }
 
+  // Where the chunks begin.  Blocks of 8-bit moments are counted from their
+  // tensor's first element, so there only the whole tensor can be aligned.
+  std::vector<int> heads(static_cast<size_t>(npieces), 0);
+  nchunks = 0;
+  for (int32_t i = 0; i < npieces; ++i) {
+    const zs_adamw_piece& q = pieces[i];
+    if (state_bits != 8) {
+      std::vector<Stream> streams;
+      const auto add = [&](const void* at, unsigned size, unsigned weight) {
+        if (at) streams.push_back({reinterpret_cast<uintptr_t>(at), size, weight});
+      };
+      for (int32_t r = 0; r < p; ++r)
+        add(q.grads[r], static_cast<unsigned>(gsize), static_cast<unsigned>(gsize));
+      if (state_bits == 32) {
+        add(q.w, 4, 8);
+        add(q.m, 4, 8);
+        add(q.v, 4, 8);
+        if (param_dtype != 0) add(q.param, 2, 2);
+      }
+      if (state_bits == 0) add(q.g_mean, 4, 4);
+      heads[static_cast<size_t>(i)] = head_of(streams);
+    }
+    nchunks += chunks_of(q.len, chunk, heads[static_cast<size_t>(i)]);
+  }
+  lay = layout(nchunks, npieces, p);
+
   std::vector<unsigned char> host(lay.partial, 0);
   auto* chunks = reinterpret_cast<zs::AwChunk*>(host.data() + lay.chunks);
   auto* gptrs = reinterpret_cast<uint64_t*>(host.data() + lay.gptrs);
@@ -147,7 +214,10 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
     const zs_adamw_piece& q = pieces[i];
     for (int32_t r = 0; r < p; ++r)
       gptrs[static_cast<int64_t>(i) * p + r] = at(q.grads[r], gsize, 0);
-    for (int64_t e = 0; e < q.len; e += chunk) {
+    const int head = heads[static_cast<size_t>(i)];
+    int64_t n = head == 0 ? chunk : chunk - kHeadMost + head;
+    for (int64_t e = 0; e < q.len; e += n, n = chunk) {
+      n = std::min(n, q.len - e);
       zs::AwChunk& d = chunks[c++];
       if (state_bits != 0) {
         d.w = at(q.w, 4, e);
@@ -165,7 +235,7 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
       d.g_mean = at(q.g_mean, 4, e);
       d.index = q.index + e;
       d.start = e;
-      d.len = static_cast<int32_t>(std::min(chunk, q.len - e));
+      d.len = static_cast<int32_t>(n);
       d.piece = i;
     }
   }

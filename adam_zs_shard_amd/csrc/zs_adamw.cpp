@@ -241,8 +241,7 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
   }
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = hipMemcpyAsync(workspace, host.data(), host.size(), hipMemcpyHostToDevice, s);
-  if (e != hipSuccess) return static_cast<zs_status>(zs::hip_status(e));
-  e = hipStreamSynchronize(s);
+  if (e == hipSuccess) e = hipStreamSynchronize(s);
   if (e != hipSuccess) return static_cast<zs_status>(zs::hip_status(e));
   table->workspace = workspace;
   table->nchunks = nchunks;
@@ -279,7 +278,7 @@ zs_status check_hparams(const zs_adamw_hparams* h) {
   return ZS_OK;
 }
 
-zs::AwConsts make_consts(const zs_adamw_hparams& h, int32_t p, int32_t bits) {
+zs::AwConsts make_consts(const zs_adamw_hparams& h) {
   zs::AwConsts c;
   const double t = static_cast<double>(h.step);
   const double bc1 = 1.0 - std::pow(h.beta1, t), bc2 = 1.0 - std::pow(h.beta2, t);
@@ -288,17 +287,27 @@ zs::AwConsts make_consts(const zs_adamw_hparams& h, int32_t p, int32_t bits) {
   c.B2 = static_cast<float>(h.beta2);
   c.C2 = static_cast<float>(1.0 - h.beta2);
   c.A1 = static_cast<float>(bc1);
-  c.A2 = static_cast<float>(bits == 32 ? bc2 : 1.0 / std::sqrt(bc2));
+  c.A2 = static_cast<float>(bc2);
+  c.R2 = static_cast<float>(1.0 / std::sqrt(bc2));
   c.EPS = static_cast<float>(h.eps);
-  c.PF = static_cast<float>(static_cast<double>(p));
-  c.lr = h.lr;
   c.inv_bc1 = 1.0 / bc1;
+  c.lr = h.lr;
   c.step = h.step;
   return c;
 }
 
-zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_hparams* hp, const double* sumsq,
-                     void* stream) {
+zs_status from_hip(hipError_t e) {
+  return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
+}
+
+zs_status check_steps(const zs_adamw_steps* s) {
+  if (!s || !s->dev) return ZS_ERR_NULL;
+  if (s->nsteps < 1 || s->nsteps > ZS_MAX_TABLE_STEPS || s->reserved != 0) return ZS_ERR_ARG;
+  return ZS_OK;
+}
+
+zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_steps* steps,
+                     const zs_adamw_hparams* hp, const double* sumsq, void* stream) {
   if (const zs_status st = check_table(t)) return st;
   if (const zs_status st = check_hparams(hp)) return st;
   if (t->state_bits == 0) return ZS_ERR_ARG;
@@ -311,21 +320,57 @@ zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_hparams* hp, const 
   L.a.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
   L.a.gptrs = reinterpret_cast<const uint64_t*>(base + lay.gptrs);
   L.a.sumsq = sumsq;
+  L.a.steps = steps ? static_cast<zs::AwStepsDev*>(steps->dev) : nullptr;
   L.a.grad_scale = hp->grad_scale;
   L.a.max_norm = hp->max_norm;
   L.a.seed = hp->seed;
   L.a.p = t->p;
   L.a.skip_nonfinite = hp->skip_nonfinite;
-  L.a.c = make_consts(*hp, t->p, t->state_bits);
   L.a.units = units_of(t->chunk_elems);
+  L.a.PF = static_cast<float>(static_cast<double>(t->p));
+  L.a.c = make_consts(*hp);
   L.nchunks = t->nchunks;
   L.gdt = t->grad_dtype;
   L.pdt = t->param_dtype ? t->param_dtype : ZS_BF16;
   L.bits = t->state_bits;
   L.rounding = hp->rounding;
   L.stream = static_cast<hipStream_t>(stream);
-  const hipError_t e = t->state_bits == 32 ? zs::launch_adamw32(L) : zs::launch_adamw8(L);
-  return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
+  return from_hip(t->state_bits == 32 ? zs::launch_adamw32(L) : zs::launch_adamw8(L));
+}
+
+size_t steps_bytes(int32_t nsteps) {
+  if (nsteps < 1 || nsteps > ZS_MAX_TABLE_STEPS) return 0;
+  return up256(sizeof(zs::AwStepsDev) + sizeof(zs::AwConsts) * static_cast<size_t>(nsteps));
+}
+
+zs_status steps_init(const zs_adamw_hparams* hp, const double* lrs, int32_t nsteps, void* dev,
+                     size_t bytes, void* stream, zs_adamw_steps* out) {
+  if (!out || !dev) return ZS_ERR_NULL;
+  if (const zs_status st = check_hparams(hp)) return st;
+  if (nsteps < 1 || nsteps > ZS_MAX_TABLE_STEPS) return ZS_ERR_ARG;
+  if (hp->step > INT64_MAX - nsteps) return ZS_ERR_RANGE;
+  for (int32_t i = 0; lrs && i < nsteps; ++i)
+    if (!std::isfinite(lrs[i])) return ZS_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(dev) % 256u != 0 || bytes < steps_bytes(nsteps))
+    return ZS_ERR_CAPACITY;
+  std::vector<unsigned char> host(steps_bytes(nsteps), 0);
+  reinterpret_cast<zs::AwStepsDev*>(host.data())->nsteps = nsteps;
+  auto* entry = reinterpret_cast<zs::AwConsts*>(host.data() + sizeof(zs::AwStepsDev));
+  zs_adamw_hparams h = *hp;
+  for (int32_t i = 0; i < nsteps; ++i) {
+    h.step = hp->step + i;
+    if (lrs) h.lr = lrs[i];
+    entry[i] = make_consts(h);
+  }
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipMemcpyAsync(dev, host.data(), host.size(), hipMemcpyHostToDevice, s);
+  if (e == hipSuccess) e = hipStreamSynchronize(s);
+  if (e != hipSuccess) return from_hip(e);
+  out->dev = dev;
+  out->first_step = hp->step;
+  out->nsteps = nsteps;
+  out->reserved = 0;
+  return ZS_OK;
 }
 
 zs_status convert_args(const float* x, const void* codes, const float* scales, int64_t n,
@@ -370,7 +415,42 @@ zs_status zs_adamw_upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t
 
 zs_status zs_adamw_step_multi(const zs_adamw_table* table, const zs_adamw_hparams* hp,
                               const double* sumsq, void* stream) {
-  return zs::guard([&] { return adamw_step(table, hp, sumsq, stream); });
+  return zs::guard([&] { return adamw_step(table, nullptr, hp, sumsq, stream); });
+}
+
+zs_status zs_adamw_step_multi_dev(const zs_adamw_table* table, const zs_adamw_steps* steps,
+                                  const zs_adamw_hparams* hp, const double* sumsq, void* stream) {
+  return zs::guard([&]() -> zs_status {
+    if (const zs_status st = check_steps(steps)) return st;
+    return adamw_step(table, steps, hp, sumsq, stream);
+  });
+}
+
+size_t zs_adamw_steps_bytes(int32_t nsteps) { return steps_bytes(nsteps); }
+
+zs_status zs_adamw_steps_init(const zs_adamw_hparams* hp, const double* lrs, int32_t nsteps,
+                              void* dev, size_t bytes, void* stream, zs_adamw_steps* steps) {
+  return zs::guard([&] { return steps_init(hp, lrs, nsteps, dev, bytes, stream, steps); });
+}
+
+zs_status zs_adamw_steps_advance(const zs_adamw_steps* steps, const double* sumsq, void* stream) {
+  if (const zs_status st = check_steps(steps)) return st;
+  if (reinterpret_cast<uintptr_t>(sumsq) % sizeof(double) != 0) return ZS_ERR_ARG;
+  return from_hip(zs::launch_steps_advance(static_cast<zs::AwStepsDev*>(steps->dev), sumsq,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+zs_status zs_adamw_steps_status(const zs_adamw_steps* steps, int64_t* cursor, int32_t* exhausted,
+                                void* stream) {
+  if (const zs_status st = check_steps(steps)) return st;
+  zs::AwStepsDev t;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = hipMemcpyAsync(&t, steps->dev, sizeof(t), hipMemcpyDeviceToHost, s);
+  if (e == hipSuccess) e = hipStreamSynchronize(s);
+  if (e != hipSuccess) return from_hip(e);
+  if (cursor) *cursor = t.cursor;
+  if (exhausted) *exhausted = t.exhausted;
+  return ZS_OK;
 }
 
 zs_status zs_grad_sumsq_multi(const zs_adamw_table* t, int32_t store_mean, int32_t accumulate,
@@ -396,8 +476,7 @@ zs_status zs_grad_sumsq_multi(const zs_adamw_table* t, int32_t store_mean, int32
     L.arrived = reinterpret_cast<unsigned int*>(base + lay.arrived);
     L.out = sumsq;
     L.stream = static_cast<hipStream_t>(stream);
-    const hipError_t e = zs::launch_sumsq(L);
-    return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
+    return from_hip(zs::launch_sumsq(L));
   });
 }
 
@@ -405,18 +484,14 @@ zs_status zs_state8_encode(const float* x, int64_t n, int32_t kind, void* codes,
                            void* stream) {
   if (const zs_status st = convert_args(x, codes, scales, n, kind)) return st;
   if (n == 0) return ZS_OK;
-  const hipError_t e = zs::launch_state8_encode(x, n, kind, codes, scales,
-                                                static_cast<hipStream_t>(stream));
-  return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
+  return from_hip(zs::launch_state8_encode(x, n, kind, codes, scales, static_cast<hipStream_t>(stream)));
 }
 
 zs_status zs_state8_decode(const void* codes, const float* scales, int64_t n, int32_t kind,
                            float* x, void* stream) {
   if (const zs_status st = convert_args(x, codes, scales, n, kind)) return st;
   if (n == 0) return ZS_OK;
-  const hipError_t e = zs::launch_state8_decode(codes, scales, n, kind, x,
-                                                static_cast<hipStream_t>(stream));
-  return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
+  return from_hip(zs::launch_state8_decode(codes, scales, n, kind, x, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

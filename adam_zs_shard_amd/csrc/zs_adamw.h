@@ -32,22 +32,36 @@ static_assert(sizeof(AwChunk) == 128, "one table entry per 128-byte line");
 // The scalars of one step, each computed in double and rounded once.
 struct AwConsts {
   float B1, C1, B2, C2;
-  float A1, A2;  // 32-bit states: 1-beta1^t, 1-beta2^t; 8-bit: A2 = 1/sqrt(1-beta2^t)
-  float EPS, PF;
+  float A1, A2;    // 1-beta1^t, 1-beta2^t (32-bit moments)
+  float R2;        // 1/sqrt(1-beta2^t) (8-bit moments)
+  float EPS;
+  double inv_bc1;  // 1/(1-beta1^t) (8-bit moments)
   double lr;
-  double inv_bc1;  // 8-bit states: 1/(1-beta1^t)
   int64_t step;
 };
+
+// A step table on the device: launches that read it apply entry `cursor`; one
+// that finds the cursor past the end does nothing and sets `exhausted`.
+struct AwStepsDev {
+  int64_t cursor;
+  int64_t nsteps;
+  int32_t exhausted;
+  int32_t reserved[11];
+  // nsteps AwConsts behind it
+};
+static_assert(sizeof(AwStepsDev) == 64, "the entries begin on a 64-byte boundary");
 
 struct AwArgs {
   const AwChunk* chunks;
   const uint64_t* gptrs;     // npieces * p rank pointers at the tensors' first elements
   const double* sumsq;       // or null
+  AwStepsDev* steps;         // or null: the constants below
   double grad_scale, max_norm;
   uint64_t seed;
   int32_t p;
   int32_t skip_nonfinite;
   int32_t units;  // per chunk, a power of two's exponent
+  float PF;       // f32(p)
   AwConsts c;
 };
 
@@ -74,6 +88,8 @@ constexpr int kSumsqBlocks = 2048;  // workgroups of a sum of squares at most
 hipError_t launch_adamw32(const AwLaunch& a);
 hipError_t launch_adamw8(const AwLaunch& a);
 hipError_t launch_sumsq(const SumsqLaunch& a);
+// cursor += 1, unless sumsq is given and not finite.
+hipError_t launch_steps_advance(AwStepsDev* t, const double* sumsq, hipStream_t stream);
 hipError_t launch_state8_encode(const float* x, int64_t n, int kind, void* codes, float* scales,
                                 hipStream_t stream);
 hipError_t launch_state8_decode(const void* codes, const float* scales, int64_t n, int kind,

@@ -412,14 +412,14 @@ struct Scalars {
 
 __device__ __forceinline__ Scalars scalars(const AwArgs& a) {
   if (!a.sumsq) return Scalars{static_cast<float>(a.grad_scale), false};
-  const double norm = __builtin_sqrt(*a.sumsq) * __builtin_fabs(a.grad_scale);
-  const bool finite = __builtin_fabs(norm) < __builtin_inf();
+  const double sumsq = *a.sumsq;
   double coef = 1.0;
   if (a.max_norm > 0.0) {
-    coef = a.max_norm / (norm + 1e-6);
+    coef = a.max_norm / (__builtin_sqrt(sumsq) * __builtin_fabs(a.grad_scale) + 1e-6);
     coef = coef > 1.0 ? 1.0 : coef;  // NaN stays
   }
-  return Scalars{static_cast<float>(a.grad_scale * coef), a.skip_nonfinite != 0 && !finite};
+  return Scalars{static_cast<float>(a.grad_scale * coef),
+                 a.skip_nonfinite != 0 && !__builtin_isfinite(sumsq)};
 }
 
 // One element's moments, in the order of the fp32 definition.

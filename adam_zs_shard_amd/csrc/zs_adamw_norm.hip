@@ -120,6 +120,10 @@ __global__ __launch_bounds__(kBlock) void sumsq_join_kernel(const double* partia
   if (threadIdx.x == 0) *out = accumulate ? *out + s : s;
 }
 
+__global__ void steps_advance_kernel(AwStepsDev* t, const double* sumsq) {
+  if (threadIdx.x == 0 && (!sumsq || __builtin_isfinite(*sumsq))) t->cursor = t->cursor + 1;
+}
+
 // One wave per block of 256 values.
 template <int KIND>
 __device__ __forceinline__ void encode_block(const float* x, int64_t n, uint8_t* codes,
@@ -211,6 +215,11 @@ hipError_t launch_sumsq(const SumsqLaunch& L) {
   if (e != hipSuccess || grid <= kJoinMost) return e;
   sumsq_join_kernel<<<dim3(1), dim3(kBlock), 0, L.stream>>>(L.partial, static_cast<int>(grid),
                                                             L.accumulate ? 1 : 0, L.out);
+  return hipGetLastError();
+}
+
+hipError_t launch_steps_advance(AwStepsDev* t, const double* sumsq, hipStream_t stream) {
+  steps_advance_kernel<<<dim3(1), dim3(kWave), 0, stream>>>(t, sumsq);
   return hipGetLastError();
 }
 

@@ -13,7 +13,8 @@ namespace {
 // whole blocks; else (U = 1) the lane's n (0..4) elements of a tensor's last
 // block.
 template <int U, int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
-__device__ __forceinline__ void step_blocks(const AwArgs& a, const Chunk& ch, float GS, float LR,
+__device__ __forceinline__ void step_blocks(const AwArgs& a, const AwConsts& c, const Chunk& ch,
+                                            float GS, float LR,
                                             float LD, int b, uint32_t lane, int n) {
   const int64_t e0 = static_cast<int64_t>(b) * kStateBlock;
   float g[U][kQuad], w[U][kQuad], m[U][kQuad], v[U][kQuad];
@@ -45,7 +46,7 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const Chunk& ch, fl
 #pragma unroll
     for (int u = 0; u < U; ++u) widen4<GDT>(gq[u], g[u]);
   } else {
-    mean_ranks<U, GDT>(rank_ptrs(a.gptrs, ch.piece, a.p), a.p, a.c.PF, ch.start + e0, lane, n, g);
+    mean_ranks<U, GDT>(rank_ptrs(a.gptrs, ch.piece, a.p), a.p, a.PF, ch.start + e0, lane, n, g);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
@@ -60,16 +61,16 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const Chunk& ch, fl
     }
 #pragma unroll
     for (int j = 0; j < kQuad; ++j) {
-      moments1(a.c, g[u][j] * GS, m[u][j], v[u][j]);
+      moments1(c, g[u][j] * GS, m[u][j], v[u][j]);
       float x;
       if constexpr (BITS == 32) {
-        x = (m[u][j] / a.c.A1) / (__builtin_sqrtf(v[u][j] / a.c.A2) + a.c.EPS);
+        x = (m[u][j] / c.A1) / (__builtin_sqrtf(v[u][j] / c.A2) + c.EPS);
       } else {
         // the hardware's root and reciprocal: the 8-bit step is as much bound
         // by its arithmetic as by HBM, and moments that are held to 2^-4 need
         // no correctly rounded quotient
         x = m[u][j] *
-            __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[u][j]) * a.c.A2 + a.c.EPS);
+            __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[u][j]) * c.R2 + c.EPS);
       }
       w[u][j] = w[u][j] - (LR * x + LD * w[u][j]);
     }
@@ -105,7 +106,7 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const Chunk& ch, fl
       uint32_t word[kQuad] = {0u, 0u, 0u, 0u};
       if constexpr (RANDOM)
         philox(static_cast<uint64_t>(ch.index + e + kQuad * lane),
-               static_cast<uint64_t>(a.c.step), a.seed, word);
+               static_cast<uint64_t>(c.step), a.seed, word);
       const uint32_t cm = encode4<ZS_STATE8_M, RANDOM>(m[u], sm, word);
       const uint32_t cv = encode4<ZS_STATE8_V, RANDOM>(v[u], sv, word);
       if (n < 0) {
@@ -133,16 +134,25 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(AwArgs a) {
   if (left <= 0) return;
   const Scalars s = scalars(a);
   if (s.skip) return;
-  const double lr = a.c.lr * ch.lr_scale;
-  const float LR = static_cast<float>(BITS == 32 ? lr : lr * a.c.inv_bc1);
+  AwConsts c = a.c;
+  if (a.steps) {
+    const int64_t at = a.steps->cursor;
+    if (at < 0 || at >= a.steps->nsteps) {
+      if (blockIdx.x == 0 && threadIdx.x == 0) a.steps->exhausted = 1;
+      return;
+    }
+    c = reinterpret_cast<const AwConsts*>(a.steps + 1)[at];
+  }
+  const double lr = c.lr * ch.lr_scale;
+  const float LR = static_cast<float>(BITS == 32 ? lr : lr * c.inv_bc1);
   const float LD = static_cast<float>(lr * ch.decay);
   const uint32_t lane = threadIdx.x % kWave;
   if (left >= kStateBlock) {
-    step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, ch, s.GS, LR, LD, b, lane, -1);
+    step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, c, ch, s.GS, LR, LD, b, lane, -1);
   } else {
     int n = left - kQuad * static_cast<int>(lane);
     n = n < 0 ? 0 : n > kQuad ? kQuad : n;
-    step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, ch, s.GS, LR, LD, b, lane, n);
+    step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, c, ch, s.GS, LR, LD, b, lane, n);
   }
 }
 

@@ -23,7 +23,8 @@ KINDS = {"m": ZS_STATE8_M, "v": ZS_STATE8_V}
 
 EXPORTS = [
     "zs_adamw_workspace_bytes", "zs_adamw_upload", "zs_adamw_step_multi", "zs_grad_sumsq_multi",
-    "zs_state8_encode", "zs_state8_decode",
+    "zs_state8_encode", "zs_state8_decode", "zs_adamw_steps_bytes", "zs_adamw_steps_init",
+    "zs_adamw_steps_advance", "zs_adamw_steps_status", "zs_adamw_step_multi_dev",
 ]
 
 
@@ -45,6 +46,11 @@ class zs_adamw_hparams(C.Structure):
                 ("eps", C.c_double), ("step", C.c_int64), ("grad_scale", C.c_double),
                 ("max_norm", C.c_double), ("seed", C.c_uint64), ("rounding", C.c_int32),
                 ("skip_nonfinite", C.c_int32)]
+
+
+class zs_adamw_steps(C.Structure):
+    _fields_ = [("dev", C.c_void_p), ("first_step", C.c_int64), ("nsteps", C.c_int32),
+                ("reserved", C.c_int32)]
 
 
 _lib = None
@@ -69,6 +75,17 @@ def lib():
         L.zs_state8_encode.restype = i32
         L.zs_state8_decode.argtypes = [vp, vp, i64, i32, vp, vp]
         L.zs_state8_decode.restype = i32
+        steps, hp = C.POINTER(zs_adamw_steps), C.POINTER(zs_adamw_hparams)
+        L.zs_adamw_steps_bytes.argtypes = [i32]
+        L.zs_adamw_steps_bytes.restype = C.c_size_t
+        L.zs_adamw_steps_init.argtypes = [hp, C.POINTER(C.c_double), i32, vp, C.c_size_t, vp, steps]
+        L.zs_adamw_steps_init.restype = i32
+        L.zs_adamw_steps_advance.argtypes = [steps, vp, vp]
+        L.zs_adamw_steps_advance.restype = i32
+        L.zs_adamw_steps_status.argtypes = [steps, C.POINTER(i64), C.POINTER(i32), vp]
+        L.zs_adamw_steps_status.restype = i32
+        L.zs_adamw_step_multi_dev.argtypes = [C.POINTER(zs_adamw_table), steps, hp, vp, vp]
+        L.zs_adamw_step_multi_dev.restype = i32
         _lib = L
     return _lib
 
@@ -123,6 +140,48 @@ def zs_adamw_step_multi(table: zs_adamw_table, hp: zs_adamw_hparams, sumsq=None,
     st = lib().zs_adamw_step_multi(C.byref(table), C.byref(hp), z._addr(sumsq), z._stream(stream))
     if check:
         z._check(st, "zs_adamw_step_multi")
+    return st
+
+
+def zs_adamw_steps_bytes(nsteps: int) -> int:
+    return lib().zs_adamw_steps_bytes(nsteps)
+
+
+def zs_adamw_steps_init(hp: zs_adamw_hparams, nsteps: int, dev, nbytes: int, *, lrs=None,
+                        stream=None) -> zs_adamw_steps:
+    """lrs: nsteps learning rates, or None for hp's at every step."""
+    if lrs is not None:
+        if len(lrs) != nsteps:
+            raise ValueError(f"{len(lrs)} learning rates for {nsteps} steps")
+        lrs = (C.c_double * max(nsteps, 1))(*lrs)
+    t = zs_adamw_steps()
+    z._check(lib().zs_adamw_steps_init(C.byref(hp), lrs, nsteps, z._addr(dev), nbytes,
+                                       z._stream(stream), C.byref(t)), "zs_adamw_steps_init")
+    return t
+
+
+def zs_adamw_steps_advance(steps: zs_adamw_steps, sumsq=None, *, stream=None, check=True) -> int:
+    st = lib().zs_adamw_steps_advance(C.byref(steps), z._addr(sumsq), z._stream(stream))
+    if check:
+        z._check(st, "zs_adamw_steps_advance")
+    return st
+
+
+def zs_adamw_steps_status(steps: zs_adamw_steps, *, stream=None):
+    """(cursor, exhausted) read back from the device."""
+    cur, ex = C.c_int64(), C.c_int32()
+    z._check(lib().zs_adamw_steps_status(C.byref(steps), C.byref(cur), C.byref(ex),
+                                         z._stream(stream)), "zs_adamw_steps_status")
+    return cur.value, ex.value
+
+
+def zs_adamw_step_multi_dev(table: zs_adamw_table, steps: zs_adamw_steps, hp: zs_adamw_hparams,
+                            sumsq=None, *, stream=None, check=True) -> int:
+    """hp: grad_scale, max_norm, seed, rounding and skip_nonfinite; the rest is the step table's."""
+    st = lib().zs_adamw_step_multi_dev(C.byref(table), C.byref(steps), C.byref(hp),
+                                       z._addr(sumsq), z._stream(stream))
+    if check:
+        z._check(st, "zs_adamw_step_multi_dev")
     return st
 
 

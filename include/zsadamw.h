@@ -128,6 +128,16 @@ typedef struct {
   int32_t skip_nonfinite; /* 1: a sumsq that is infinite or NaN leaves everything as it is (needs sumsq) */
 } zs_adamw_hparams;
 
+/* The constants of a run of steps in device memory, for launches that are
+ * captured once and replayed (compare zs_step_table): entry i holds step
+ * first_step + i, whose learning rate may follow a schedule. */
+typedef struct {
+  void* dev;
+  int64_t first_step;
+  int32_t nsteps;
+  int32_t reserved; /* 0 */
+} zs_adamw_steps;
+
 /* One AdamW step over every tensor of the table, in one launch.  sumsq: a
  * device double, the sum of squares of the whole model's mean gradient before
  * grad_scale (zs_grad_sumsq_multi, summed over the shards), or NULL.
@@ -136,6 +146,36 @@ typedef struct {
  * Errors: ZS_ERR_NULL, ZS_ERR_ARG, ZS_ERR_DTYPE, ZS_ERR_HIP. */
 zs_status zs_adamw_step_multi(const zs_adamw_table* table, const zs_adamw_hparams* hp,
                               const double* sumsq, void* stream);
+
+/* zs_adamw_step_multi with lr, beta1, beta2, eps and step from the step table's
+ * current entry, read on the device (hp's own are still checked; the rest of
+ * hp holds as there).  Captured as [zs_grad_sumsq_multi, this,
+ * zs_adamw_steps_advance], a graph replays consecutive steps.  Past the
+ * table's end nothing is updated and its `exhausted` is set. */
+zs_status zs_adamw_step_multi_dev(const zs_adamw_table* table, const zs_adamw_steps* steps,
+                                  const zs_adamw_hparams* hp, const double* sumsq, void* stream);
+
+/* Device bytes of a step table of nsteps entries (0 if nsteps is outside
+ * 1..ZS_MAX_TABLE_STEPS). */
+size_t zs_adamw_steps_bytes(int32_t nsteps);
+
+/* Fills a step table for steps hp->step .. hp->step + nsteps - 1 with hp's
+ * betas and eps and, per step, lrs[i] (a host array) or, if lrs is NULL, hp's
+ * lr; cursor 0.  dev: caller's device memory, 256-byte aligned.  One copy on
+ * `stream`, waited for: call it before capture.  Errors: ZS_ERR_NULL,
+ * ZS_ERR_ARG, ZS_ERR_RANGE, ZS_ERR_CAPACITY, ZS_ERR_HIP, ZS_ERR_RESOURCE. */
+zs_status zs_adamw_steps_init(const zs_adamw_hparams* hp, const double* lrs, int32_t nsteps,
+                              void* dev, size_t bytes, void* stream, zs_adamw_steps* steps);
+
+/* The next entry, as a one-wave kernel on `stream` (capturable).  sumsq: the
+ * norm that the step was given, or NULL; where it is infinite or NaN the
+ * cursor stays, so that a step that skip_nonfinite left out is not counted. */
+zs_status zs_adamw_steps_advance(const zs_adamw_steps* steps, const double* sumsq, void* stream);
+
+/* Reads the cursor and the exhausted flag back to the host (one copy on
+ * `stream`, waited for). */
+zs_status zs_adamw_steps_status(const zs_adamw_steps* steps, int64_t* cursor, int32_t* exhausted,
+                                void* stream);
 
 /* *sumsq = (accumulate ? *sumsq : 0) + the sum over all elements of the square
  * of the fp32 rank mean of the gradients, in double, in an order that is fixed

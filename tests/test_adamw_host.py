@@ -257,3 +257,45 @@ def test_reference_step_is_torch_adamw():
         # torch decays first and moves then: lr^2 * decay * u apart
         assert np.all(np.abs(p.detach().numpy() - w64) <= t * 1e-3 * 1e-3 * 0.1 * 12)
         assert np.all(np.abs(w - w64) <= slack)
+
+
+@no_device
+def test_step_tables_refuse():
+    hp = a.hparams(**HP)
+    assert a.zs_adamw_steps_bytes(0) == a.zs_adamw_steps_bytes(z.ZS_MAX_TABLE_STEPS + 1) == 0
+    assert a.zs_adamw_steps_bytes(1) % 256 == 0 and a.zs_adamw_steps_bytes(1000) >= 1000 * 56
+
+    def init(hp=hp, n=10, dev=FAKE, nb=1 << 16, **k):
+        try:
+            a.zs_adamw_steps_init(hp, n, dev, nb, stream=0, **k)
+        except z.ZsError as e:
+            return e.status
+        return z.ZS_OK
+
+    assert init(n=0) == init(n=-1) == init(n=z.ZS_MAX_TABLE_STEPS + 1) == z.ZS_ERR_ARG
+    assert init(a.hparams(**{**HP, "beta2": 1.0})) == z.ZS_ERR_ARG
+    assert init(a.hparams(**{**HP, "step": 2**63 - 5})) == z.ZS_ERR_RANGE
+    assert init(dev=None) == z.ZS_ERR_NULL and init(dev=FAKE + 64) == z.ZS_ERR_CAPACITY
+    assert init(nb=a.zs_adamw_steps_bytes(10) - 1) == z.ZS_ERR_CAPACITY
+    assert init(n=2, lrs=[1e-3, float("nan")]) == z.ZS_ERR_ARG
+    with pytest.raises(ValueError):
+        init(n=3, lrs=[1e-3])
+
+    def steps(**over):
+        s = a.zs_adamw_steps(FAKE, 1, 10, 0)
+        for k, x in over.items():
+            setattr(s, k, x)
+        return s
+
+    for over, st in ((dict(dev=None), z.ZS_ERR_NULL), (dict(nsteps=0), z.ZS_ERR_ARG),
+                     (dict(reserved=1), z.ZS_ERR_ARG)):
+        s = steps(**over)
+        assert a.zs_adamw_steps_advance(s, stream=0, check=False) == st
+        assert a.zs_adamw_step_multi_dev(_table(), s, hp, stream=0, check=False) == st
+        with pytest.raises(z.ZsError):
+            a.zs_adamw_steps_status(s, stream=0)
+    assert a.zs_adamw_steps_advance(steps(), FAKE + 4, stream=0, check=False) == z.ZS_ERR_ARG
+    assert a.zs_adamw_step_multi_dev(_table(state_bits=0), steps(), hp, stream=0,
+                                     check=False) == z.ZS_ERR_ARG
+    assert a.zs_adamw_step_multi_dev(_table(), steps(), a.hparams(**HP, max_norm=1.0), stream=0,
+                                     check=False) == z.ZS_ERR_NULL

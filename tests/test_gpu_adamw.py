@@ -570,3 +570,45 @@ def test_offsets_beyond_32_bits(bits):
     want = want + g[n // 1024 * 1024:].double().square().sum()
     # squares of bf16 are exact in fp32, the sums are in double
     assert abs(out.item() - want.item()) <= 1e-10 * want.item()
+
+
+@pytest.mark.parametrize("bits,rounding", [(32, "nearest"), (8, "stochastic")])
+def test_captured_steps_follow_a_step_table(bits, rounding):
+    """A graph of norm, step and advance, replayed with eager work between:
+    each replay the next step of a learning-rate schedule; a step whose norm is
+    not finite changes and counts nothing; past the end nothing moves."""
+    lens = [5000, 300, 30_001]
+    M, E = (Model(lens, 2, "bf16", "bf16", bits, seed=80) for _ in range(2))
+    lrs = [1e-3 / k for k in (1, 2, 3, 4, 5)]
+    kw = dict(max_norm=0.05, rounding=rounding, seed=9, skip_nonfinite=True)
+    hp = a.hparams(1.0, B1, B2, EPS, 41, **kw)
+    buf = torch.empty(a.zs_adamw_steps_bytes(len(lrs)), dtype=torch.uint8, device=DEV)
+    steps = a.zs_adamw_steps_init(hp, len(lrs), buf, buf.numel(), lrs=lrs)
+    sums = [torch.zeros((), dtype=torch.float64, device=DEV) for _ in range(2)]
+    graph = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph):
+            a.zs_grad_sumsq_multi(M.table, sums[0])
+            a.zs_adamw_step_multi_dev(M.table, steps, hp, sums[0])
+            a.zs_adamw_steps_advance(steps, sums[0])
+    torch.cuda.current_stream().wait_stream(side)
+    done = 0
+    for i in range(8):
+        E.draw()
+        if i == 2:
+            E.g[1][2][7] = float("inf")
+        for x, y in zip(M.g, E.g):
+            x.flat.copy_(y.flat)
+        graph.replay()
+        a.zs_grad_sumsq_multi(E.table, sums[1])
+        if i != 2 and done < len(lrs):
+            a.zs_adamw_step_multi(E.table, a.hparams(lrs[done], B1, B2, EPS, 41 + done, **kw), sums[1])
+            done += 1
+        cursor, exhausted = a.zs_adamw_steps_status(steps)
+        # an advance past the end still moves the cursor, as zs_step_table_advance's does
+        assert cursor == (i + 1 if i < 2 else i) and exhausted == (1 if i >= 6 else 0)
+        for x, y in zip(M.all(), E.all()):
+            assert np.array_equal(bits_of(x.flat), bits_of(y.flat)), f"replay {i}"
+    assert done == len(lrs)

@@ -468,6 +468,7 @@ zs_status zs_grad_sumsq_multi(const zs_adamw_table* t, int32_t store_mean, int32
     L.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
     L.gptrs = reinterpret_cast<const uint64_t*>(base + lay.gptrs);
     L.nchunks = t->nchunks;
+    L.units = units_of(t->chunk_elems);
     L.p = t->p;
     L.gdt = t->grad_dtype;
     L.store = store_mean != 0;

@@ -62,30 +62,38 @@ __device__ __forceinline__ void sumsq_blocks(const Chunk& ch, const uint64_t* gp
 // launches of at most kJoinMost workgroups do it; the others join in a
 // second launch.
 constexpr int kJoinMost = 64;
+
+// One rank: four blocks per wave and turn, so that as many bytes are in
+// flight, four workgroups per CU (1.0e9 bf16 elements 299 us, 6.7 TB/s; two,
+// three and five 300 / 333 / 298, eight blocks 325, two 365).  More ranks: one
+// block of each, three workgroups per CU, so that the window swept at a time
+// stays narrow (60M elements, 8 ranks, the mean kept: 198 us, 6.05 TB/s; two,
+// four, five and eight 229 / 208 / 225 / 222, four blocks 214).
+constexpr int kLogOne = 2;
+constexpr int kLoadsOne = 1 << kLogOne;
+constexpr int kGroupsOne = 4, kGroupsRanks = 3;
 template <int GDT, bool STORE, bool ONE, bool JOIN>
 __global__ __launch_bounds__(kBlock) void sumsq_kernel(const AwChunk* chunks,
-                                                       const uint64_t* gptrs, int64_t nchunks,
-                                                       int p, float PF, double* partial,
+                                                       const uint64_t* gptrs, int64_t nunits,
+                                                       int units, int p, float PF, double* partial,
                                                        unsigned int* arrived, int accumulate,
                                                        double* out) {
-  constexpr int U = 4;
+  constexpr int U = ONE ? kLoadsOne : 1;
   const uint32_t lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   double acc = 0.0;
-  for (int64_t c = blockIdx.x; c < nchunks; c += gridDim.x) {
-    const Chunk ch = ld_chunk(chunks + c);
-    const int full = ch.len / kStateBlock;
-    const int blocks = (ch.len + kStateBlock - 1) / kStateBlock;
-    for (int b = wave * U; b < blocks; b += kWaves * U) {
-      if (b + U <= full) {
-        sumsq_blocks<U, GDT, STORE, ONE>(ch, gptrs, p, PF, b, lane, -1, acc);
-      } else {
-        for (int k = b; k < b + U && k < blocks; ++k) {
-          int n = ch.len - k * kStateBlock - kQuad * static_cast<int>(lane);
-          n = n < 0 ? 0 : n > kQuad ? kQuad : n;
-          sumsq_blocks<1, GDT, STORE, ONE>(ch, gptrs, p, PF, k, lane, n, acc);
-        }
-      }
+  for (int64_t i = blockIdx.x; i < nunits; i += gridDim.x) {
+    const Chunk ch = ld_chunk(chunks + (i >> units));
+    const int b = (static_cast<int>(i & ((1 << units) - 1)) * kWaves + wave) * U;
+    const int left = ch.len - b * kStateBlock;
+    if (left >= U * kStateBlock) {
+      sumsq_blocks<U, GDT, STORE, ONE>(ch, gptrs, p, PF, b, lane, -1, acc);
+      continue;
+    }
+    for (int k = 0; k < U && k * kStateBlock < left; ++k) {
+      int n = left - k * kStateBlock - kQuad * static_cast<int>(lane);
+      n = n < 0 ? 0 : n > kQuad ? kQuad : n;
+      sumsq_blocks<1, GDT, STORE, ONE>(ch, gptrs, p, PF, b + k, lane, n, acc);
     }
   }
   const double s = block_sum(acc);
@@ -189,9 +197,14 @@ unsigned convert_grid(int64_t n) {
 }  // namespace
 
 hipError_t launch_sumsq(const SumsqLaunch& L) {
-  int64_t grid = static_cast<int64_t>(cu_count()) * 4;
+  const bool one = L.p == 1;
+  // a small table's entries are single units: then a wave of one rank's kernel
+  // finds blocks for one load only
+  const int units = one ? (L.units >= kLogOne ? L.units - kLogOne : 0) : L.units;
+  const int64_t nunits = L.nchunks << units;
+  int64_t grid = static_cast<int64_t>(cu_count()) * (one ? kGroupsOne : kGroupsRanks);
   if (grid > kSumsqBlocks) grid = kSumsqBlocks;
-  if (grid > L.nchunks) grid = L.nchunks;
+  if (grid > nunits) grid = nunits;
   if (grid < 1) grid = 1;  // no tensors: the sum is still written
   const float PF = static_cast<float>(static_cast<double>(L.p));
   with_gdt(L.gdt, [&](auto G) {
@@ -200,7 +213,7 @@ hipError_t launch_sumsq(const SumsqLaunch& L) {
     const auto go = [&](auto store, auto one, auto join) {
       sumsq_kernel<GDT, decltype(store)::value != 0, decltype(one)::value != 0,
                    decltype(join)::value != 0>
-          <<<gd, bd, 0, L.stream>>>(L.chunks, L.gptrs, L.nchunks, L.p, PF, L.partial, L.arrived,
+          <<<gd, bd, 0, L.stream>>>(L.chunks, L.gptrs, nunits, units, L.p, PF, L.partial, L.arrived,
                                     L.accumulate ? 1 : 0, L.out);
     };
     const auto go2 = [&](auto store, auto one) {

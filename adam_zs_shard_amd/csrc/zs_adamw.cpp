@@ -14,8 +14,7 @@
 namespace {
 
 constexpr int64_t kMaxLen = int64_t{1} << 60;
-// A launch counts its lanes in 32 bits: 2^24 workgroups of 256 at most.
-constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
+using zs::kMaxGroups;
 
 // Elements per entry of the launch table, in units of one workgroup.
 constexpr int kUnitsLarge = 3, kUnitsSmall = 0;

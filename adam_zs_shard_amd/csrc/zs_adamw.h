@@ -7,6 +7,8 @@
 namespace zs {
 
 constexpr int kF32 = ZS_F32;
+// A launch counts its lanes in 32 bits: 2^24 workgroups of 256 at most.
+constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
 constexpr int kStateBlock = ZS_STATE8_BLOCK;  // one wave: 64 lanes x 4 elements
 
 // A run of at most chunk_elems elements of one tensor, with every address at

@@ -75,13 +75,13 @@ struct Raw4<kF32> {
 template <int DT>
 constexpr int kSize = DT == kF32 ? 4 : 2;
 
-template <int DT>
+// Non-temporal unless STREAM is false.
+template <int DT, bool STREAM = true>
 __device__ __forceinline__ Raw4<DT> ld_raw4(const void* base, uint32_t lane) {
-  const char* p = static_cast<const char*>(base) + lane * (kQuad * kSize<DT>);
-  if constexpr (DT == kF32)
-    return Raw4<DT>{__builtin_nontemporal_load(reinterpret_cast<const f32x4*>(p))};
-  else
-    return Raw4<DT>{__builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p))};
+  using T = std::conditional_t<DT == kF32, f32x4, u32x2>;
+  const T* p = reinterpret_cast<const T*>(static_cast<const char*>(base) +
+                                          lane * (kQuad * kSize<DT>));
+  return Raw4<DT>{STREAM ? __builtin_nontemporal_load(p) : *p};
 }
 // The first n (0..4) of the lane's elements, zeros behind them.
 template <int DT>
@@ -138,10 +138,12 @@ __device__ __forceinline__ void st_quad16(uint16_t* base, uint32_t lane, int n,
   for (int j = 0; j < kQuad; ++j)
     if (j < n) base[lane * kQuad + j] = narrow1<DT>(x[j]);
 }
-// Four codes, one per byte.
+// Four codes, one per byte.  Plain loads: a wave's 256 bytes of codes that do
+// not begin on a line share theirs with the next wave's, which non-temporal
+// loads fetched twice (4.0e8 elements in buffers 3 elements into a line 1.22
+// -> 1.16 ms; on a line 1.03 either way).
 __device__ __forceinline__ uint32_t ld_codes(const void* base, uint32_t lane) {
-  return __builtin_nontemporal_load(
-      reinterpret_cast<const u32b*>(static_cast<const char*>(base) + lane * kQuad));
+  return *reinterpret_cast<const u32b*>(static_cast<const char*>(base) + lane * kQuad);
 }
 __device__ __forceinline__ uint32_t ld_codes(const void* base, uint32_t lane, int n) {
   const uint8_t* p = static_cast<const uint8_t*>(base) + lane * kQuad;

@@ -56,12 +56,15 @@ __device__ __forceinline__ void sumsq_blocks(const Chunk& ch, const uint64_t* gp
 
 // Joining the workgroups' sums.  JOIN: the last workgroup to arrive adds them
 // up, in their order whoever it is, and makes the count ready for the next
-// launch.  That saves a launch (8 -> 5 us of the host's time for 50,000
-// elements), but each arrival writes back and invalidates its L2: with 1024
-// workgroups it cost 40 us (15.6M elements, 8 ranks: 62 -> 105 us), so only
-// launches of at most kJoinMost workgroups do it; the others join in a
-// second launch.
+// launch.  That saves a launch (6.9 -> 4.6 us of the host's time), but each
+// arrival writes back and invalidates its L2: with 1024 workgroups it cost 40
+// us (15.6M elements, 8 ranks: 62 -> 105 us), so only launches of at most
+// kJoinMost workgroups do it, and tables of so few units that as many can
+// read them as fast (500,000 elements 4.8 us on the GPU, 5.2 with a workgroup
+// per unit and a second launch; with twice the units 7.7 and 5.6); the others
+// join in a second launch.
 constexpr int kJoinMost = 64;
+constexpr int64_t kJoinUnits = 8 * kJoinMost;  // times ranks
 
 // One rank: four blocks per wave and turn, so that as many bytes are in
 // flight, four workgroups per CU (1.0e9 bf16 elements 299 us, 6.7 TB/s; two,
@@ -72,13 +75,12 @@ constexpr int kJoinMost = 64;
 constexpr int kLogOne = 2;
 constexpr int kLoadsOne = 1 << kLogOne;
 constexpr int kGroupsOne = 4, kGroupsRanks = 3;
-template <int GDT, bool STORE, bool ONE, bool JOIN>
+template <int U, int GDT, bool STORE, bool ONE, bool JOIN>
 __global__ __launch_bounds__(kBlock) void sumsq_kernel(const AwChunk* chunks,
                                                        const uint64_t* gptrs, int64_t nunits,
                                                        int units, int p, float PF, double* partial,
                                                        unsigned int* arrived, int accumulate,
                                                        double* out) {
-  constexpr int U = ONE ? kLoadsOne : 1;
   const uint32_t lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   double acc = 0.0;
@@ -199,12 +201,12 @@ unsigned convert_grid(int64_t n) {
 }  // namespace
 
 hipError_t launch_sumsq(const SumsqLaunch& L) {
-  const bool one = L.p == 1;
-  // a small table's entries are single units: then a wave of one rank's kernel
-  // finds blocks for one load only
-  const int units = one ? (L.units >= kLogOne ? L.units - kLogOne : 0) : L.units;
+  // entries of a small table are single units, which feed one block per wave
+  const bool four = L.p == 1 && L.units >= kLogOne;
+  const int units = four ? L.units - kLogOne : L.units;
   const int64_t nunits = L.nchunks << units;
-  int64_t grid = static_cast<int64_t>(cu_count()) * (one ? kGroupsOne : kGroupsRanks);
+  int64_t grid = static_cast<int64_t>(cu_count()) * (L.p == 1 ? kGroupsOne : kGroupsRanks);
+  if (nunits * L.p <= kJoinUnits) grid = kJoinMost;
   if (grid > kSumsqBlocks) grid = kSumsqBlocks;
   if (grid > nunits) grid = nunits;
   if (grid < 1) grid = 1;  // no tensors: the sum is still written
@@ -212,19 +214,23 @@ hipError_t launch_sumsq(const SumsqLaunch& L) {
   with_gdt(L.gdt, [&](auto G) {
     constexpr int GDT = decltype(G)::value;
     const dim3 gd(static_cast<unsigned>(grid)), bd(kBlock);
-    const auto go = [&](auto store, auto one, auto join) {
-      sumsq_kernel<GDT, decltype(store)::value != 0, decltype(one)::value != 0,
-                   decltype(join)::value != 0>
-          <<<gd, bd, 0, L.stream>>>(L.chunks, L.gptrs, nunits, units, L.p, PF, L.partial, L.arrived,
-                                    L.accumulate ? 1 : 0, L.out);
+    const auto go = [&](auto u, auto store, auto one, auto join) {
+      sumsq_kernel<decltype(u)::value, GDT, decltype(store)::value != 0,
+                   decltype(one)::value != 0, decltype(join)::value != 0>
+          <<<gd, bd, 0, L.stream>>>(L.chunks, L.gptrs, nunits, units, L.p, PF, L.partial,
+                                    L.arrived, L.accumulate ? 1 : 0, L.out);
     };
-    const auto go2 = [&](auto store, auto one) {
-      grid <= kJoinMost ? go(store, one, IC<1>{}) : go(store, one, IC<0>{});
+    const auto pick = [&](auto store) {
+      const bool join = grid <= kJoinMost;
+      if (four)
+        join ? go(IC<kLoadsOne>{}, store, IC<1>{}, IC<1>{})
+             : go(IC<kLoadsOne>{}, store, IC<1>{}, IC<0>{});
+      else if (L.p == 1)
+        join ? go(IC<1>{}, store, IC<1>{}, IC<1>{}) : go(IC<1>{}, store, IC<1>{}, IC<0>{});
+      else
+        join ? go(IC<1>{}, store, IC<0>{}, IC<1>{}) : go(IC<1>{}, store, IC<0>{}, IC<0>{});
     };
-    if (L.store)
-      L.p == 1 ? go2(IC<1>{}, IC<1>{}) : go2(IC<1>{}, IC<0>{});
-    else
-      L.p == 1 ? go2(IC<0>{}, IC<1>{}) : go2(IC<0>{}, IC<0>{});
+    L.store ? pick(IC<1>{}) : pick(IC<0>{});
   });
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || grid <= kJoinMost) return e;

@@ -325,7 +325,7 @@ zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_steps* steps,
   L.a.seed = hp->seed;
   L.a.p = t->p;
   L.a.skip_nonfinite = hp->skip_nonfinite;
-  L.a.units = units_of(t->chunk_elems);
+  L.log_blocks = units_of(t->chunk_elems) + zs::log2_of(zs::kUnit / zs::kStateBlock);
   L.a.PF = static_cast<float>(static_cast<double>(t->p));
   L.a.c = make_consts(*hp);
   L.nchunks = t->nchunks;

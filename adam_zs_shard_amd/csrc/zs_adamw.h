@@ -13,8 +13,7 @@ constexpr int kStateBlock = ZS_STATE8_BLOCK;  // one wave: 64 lanes x 4 elements
 
 // A run of at most chunk_elems elements of one tensor, with every address at
 // its first element, so that a wave knows all it needs after one scalar load.
-// Its workgroups take kUnit elements each.
-constexpr int kUnit = 4 * kStateBlock;
+constexpr int kUnit = 4 * kStateBlock;  // one workgroup of four waves
 struct AwChunk {
   uint64_t w, m, v;           // addresses as numbers, see ld_chunk
   uint64_t m_scale, v_scale;
@@ -62,14 +61,17 @@ struct AwArgs {
   uint64_t seed;
   int32_t p;
   int32_t skip_nonfinite;
-  int32_t units;  // per chunk, a power of two's exponent
+  int32_t shift;  // workgroups per chunk, a power of two's exponent
   float PF;       // f32(p)
   AwConsts c;
 };
 
+constexpr int log2_of(int x) { return x <= 1 ? 0 : 1 + log2_of(x / 2); }
+
 struct AwLaunch {
   AwArgs a;
   int64_t nchunks;
+  int log_blocks;  // blocks of 256 elements per chunk, a power of two's exponent
   int gdt, pdt, bits, rounding;
   hipStream_t stream;
 };

@@ -125,15 +125,17 @@ __device__ __forceinline__ void step_blocks(const AwArgs& a, const AwConsts& c, 
   }
 }
 
-// One workgroup per kUnit elements, one block per wave.  The grid sweeps the
-// tensors in order, so what is in flight at any moment is a narrow window of
-// each array: 1.0e9 elements with 32-bit moments take 4.96 ms this way, 5.12
-// with 2048 elements per workgroup, 5.35 with 8192.
-template <int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
-__global__ __launch_bounds__(kBlock) void adamw_kernel(AwArgs a) {
-  const Chunk ch = ld_chunk(a.chunks + (blockIdx.x >> a.units));
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int b = static_cast<int>(blockIdx.x & ((1u << a.units) - 1u)) * kWaves + wave;
+// One block per wave, W waves per workgroup.  The grid sweeps the tensors in
+// order, so what is in flight at any moment is a narrow window of each array;
+// launch_step says which W keeps it narrowest.  (1.0e9 elements with 32-bit
+// moments and four waves: 4.96 ms this way, 5.12 with two blocks per wave,
+// 5.35 with eight; 8-bit moments and two waves: 2.53, 2.91 with two, 2.98
+// with four.)
+template <int W, int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
+__global__ __launch_bounds__(W * kWave) void adamw_kernel(AwArgs a) {
+  const Chunk ch = ld_chunk(a.chunks + (blockIdx.x >> a.shift));
+  const int wave = W == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int b = static_cast<int>(blockIdx.x & ((1u << a.shift) - 1u)) * W + wave;
   const int left = ch.len - b * kStateBlock;
   if (left <= 0) return;
   const Scalars s = scalars(a);
@@ -160,25 +162,50 @@ __global__ __launch_bounds__(kBlock) void adamw_kernel(AwArgs a) {
   }
 }
 
-// LDS that the 32-bit step asks for and leaves alone: a fifth of a CU's 160
-// KiB, so that five workgroups share a CU instead of eight.  Fewer waves in
-// flight keep the sweep's window on HBM narrower: 1.0e9 elements 4.93 ms
-// without, 4.77 / 4.76 / 4.75 / 4.85 with four, five, six and seven; 20M
-// elements 91.5 -> 89.4 us.  The 8-bit step, which computes more per byte,
-// needs the waves (2.63 ms with eight, 2.98 with five).
-constexpr unsigned kReserve = 160 * 1024 / 5 - 64;
+// Waves per workgroup, and LDS that a 32-bit step asks for and leaves alone so
+// that 16 waves share a CU instead of 32.  All figures with input sets that
+// take turns, as a training step's do; 1.0e9 elements except where stated.
+// 32-bit moments, one gradient: single waves, 16 of them: 4.33-4.38 ms (6.4-6.5
+// TB/s); 12 / 14 / 20 / 24 / 32 per CU 4.78 / 4.61 / 4.43 / 4.54 / 4.68, two
+// waves per workgroup 4.47-4.49, four 4.63, eight 4.77.
+// 32-bit moments, several gradients: eight waves, two such workgroups on a CU:
+// 15.6M elements and 8 ranks 105.6 us (four waves 107.6, sixteen 112); from
+// kManyRanks on four waves, two such: 30M elements and 16 ranks 273 us against
+// 292, 15M and 64 ranks 399 against 423.
+// 8-bit moments: eight waves, as many as fit (they compute more per byte): 2.57
+// ms (two 2.53, four 2.56), buffers that begin inside a line 2.80 (3.24, 2.99);
+// 15.6M elements and 8 ranks 85.0 us (four 88.3, two 92.2).
+// A small table's chunks have four blocks, which is four waves at most.
+constexpr unsigned kReserveOne = 160 * 1024 / 16 - 64, kReserveRanks = 160 * 1024 / 2 - 64;
+constexpr int kManyRanks = 16;
 
 template <int BITS, bool RANDOM>
 void launch_step(const AwLaunch& L) {
   with_gdt(L.gdt, [&](auto G) {
     with_dt(L.pdt, [&](auto H) {
       constexpr int GDT = decltype(G)::value, PDT = decltype(H)::value;
-      const dim3 grid(static_cast<unsigned>(L.nchunks << L.a.units)), block(kBlock);
-      constexpr unsigned lds = BITS == 32 ? kReserve : 0;
-      if (L.a.p == 1)
-        adamw_kernel<GDT, PDT, BITS, RANDOM, true><<<grid, block, lds, L.stream>>>(L.a);
-      else
-        adamw_kernel<GDT, PDT, BITS, RANDOM, false><<<grid, block, lds, L.stream>>>(L.a);
+      const auto go = [&](auto waves, auto one, unsigned lds) {
+        constexpr int W = decltype(waves)::value;
+        AwArgs a = L.a;
+        a.shift = L.log_blocks - log2_of(W);
+        adamw_kernel<W, GDT, PDT, BITS, RANDOM, decltype(one)::value != 0>
+            <<<dim3(static_cast<unsigned>(L.nchunks << a.shift)), dim3(W * kWave), lds,
+               L.stream>>>(a);
+      };
+      const bool small = L.log_blocks < log2_of(8);
+      if constexpr (BITS == 32) {
+        const unsigned lds = small ? 0 : kReserveRanks;
+        if (L.a.p == 1)
+          go(IC<1>{}, IC<1>{}, kReserveOne);
+        else if (small || L.a.p >= kManyRanks)
+          go(IC<4>{}, IC<0>{}, lds);
+        else
+          go(IC<8>{}, IC<0>{}, lds);
+      } else if (L.a.p == 1) {
+        small ? go(IC<4>{}, IC<1>{}, 0) : go(IC<8>{}, IC<1>{}, 0);
+      } else {
+        small ? go(IC<4>{}, IC<0>{}, 0) : go(IC<8>{}, IC<0>{}, 0);
+      }
     });
   });
 }

@@ -134,68 +134,115 @@ __global__ void steps_advance_kernel(AwStepsDev* t, const double* sumsq) {
   if (threadIdx.x == 0 && (!sumsq || __builtin_isfinite(*sumsq))) t->cursor = t->cursor + 1;
 }
 
-// One wave per block of 256 values.
-template <int KIND>
-__device__ __forceinline__ void encode_block(const float* x, int64_t n, uint8_t* codes,
-                                             float* scales, int64_t b, uint32_t lane) {
-  const int64_t e = b * kStateBlock;
-  const int64_t left = n - e - kQuad * lane;
-  const int k = left < 0 ? 0 : left > kQuad ? kQuad : static_cast<int>(left);
-  float y[kQuad];
-  widen4<kF32>(n - e >= kStateBlock ? ld_raw4<kF32>(x + e, lane) : ld_raw4<kF32>(x + e, lane, k),
-               y);
-  uint32_t most = 0;
+// Conversions: a wave takes U blocks of 256 values, its loads first.  Two where
+// there are enough for all CUs' waves: 117M values to 8 bits 93 us, 6.3 TB/s
+// (one 102, four 92), 1.0e9 from 8 bits 800 us (919, 963); one below
+// kConvertFew values: 50,000 from 8 bits 2.2 us (two 3.0).
+constexpr int kConvertWaves = 8;
+constexpr int64_t kConvertFew = int64_t{1} << 21;
+
+template <int U, int KIND>
+__device__ __forceinline__ void encode_blocks(const float* x, uint8_t* codes, float* scales,
+                                              int64_t b, uint32_t lane, int n) {
+  Raw4<kF32> q[U];
 #pragma unroll
-  for (int j = 0; j < kQuad; ++j) most = mag_bits(y[j]) > most ? mag_bits(y[j]) : most;
-  const BlockScale s = block_scale<KIND>(wave_max(most));
-  const uint32_t none[kQuad] = {0u, 0u, 0u, 0u};
-  const uint32_t c = encode4<KIND, false>(y, s, none);
-  if (n - e >= kStateBlock)
-    st_codes(codes + e, lane, c);
-  else
-    st_codes(codes + e, lane, k, c);
-  if (lane == 0) scales[b] = s.scale;
+  for (int u = 0; u < U; ++u) {
+    const float* at = x + (b + u) * kStateBlock;
+    q[u] = n < 0 ? ld_raw4<kF32>(at, lane) : ld_raw4<kF32>(at, lane, n);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float y[kQuad];
+    widen4<kF32>(q[u], y);
+    uint32_t most = 0;
+#pragma unroll
+    for (int j = 0; j < kQuad; ++j) most = mag_bits(y[j]) > most ? mag_bits(y[j]) : most;
+    const BlockScale s = block_scale<KIND>(wave_max(most));
+    const uint32_t none[kQuad] = {0u, 0u, 0u, 0u};
+    const uint32_t c = encode4<KIND, false>(y, s, none);
+    uint8_t* to = codes + (b + u) * kStateBlock;
+    if (n < 0)
+      st_codes(to, lane, c);
+    else
+      st_codes(to, lane, n, c);
+    if (lane == 0) scales[b + u] = s.scale;
+  }
 }
 
-template <int KIND>
-__device__ __forceinline__ void decode_block(const uint8_t* codes, const float* scales, int64_t n,
-                                             float* x, int64_t b, uint32_t lane) {
-  const int64_t e = b * kStateBlock;
-  const int64_t left = n - e - kQuad * lane;
-  const int k = left < 0 ? 0 : left > kQuad ? kQuad : static_cast<int>(left);
-  float y[kQuad];
-  decode4<KIND>(n - e >= kStateBlock ? ld_codes(codes + e, lane) : ld_codes(codes + e, lane, k),
-                scales[b], y);
-  if (n - e >= kStateBlock)
-    st_quad32(x + e, lane, y);
-  else
-    st_quad32(x + e, lane, k, y);
+template <int U, int KIND>
+__device__ __forceinline__ void decode_blocks(const uint8_t* codes, const float* scales, float* x,
+                                              int64_t b, uint32_t lane, int n) {
+  uint32_t c[U];
+  float s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const uint8_t* at = codes + (b + u) * kStateBlock;
+    c[u] = n < 0 ? ld_codes(at, lane) : ld_codes(at, lane, n);
+    s[u] = scales[b + u];
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float y[kQuad];
+    decode4<KIND>(c[u], s[u], y);
+    float* to = x + (b + u) * kStateBlock;
+    if (n < 0)
+      st_quad32(to, lane, y);
+    else
+      st_quad32(to, lane, n, y);
+  }
 }
 
-template <int KIND>
-__global__ __launch_bounds__(kBlock) void encode_kernel(const float* x, int64_t n, uint8_t* codes,
-                                                        float* scales) {
+// Calls f(U blocks, first block, values of this lane or -1) for the wave's
+// blocks of n values.
+template <int U, class F>
+__device__ __forceinline__ void convert_all(int64_t n, F&& f) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  for (int64_t b = static_cast<int64_t>(blockIdx.x) * kWaves + wave; b * kStateBlock < n;
-       b += static_cast<int64_t>(gridDim.x) * kWaves)
-    encode_block<KIND>(x, n, codes, scales, b, threadIdx.x % kWave);
+  const int64_t whole = n / kStateBlock, blocks = (n + kStateBlock - 1) / kStateBlock;
+  for (int64_t b = (static_cast<int64_t>(blockIdx.x) * kConvertWaves + wave) * U; b < blocks;
+       b += static_cast<int64_t>(gridDim.x) * kConvertWaves * U) {
+    if (b + U <= whole) {
+      f(IC<U>{}, b, -1);
+      continue;
+    }
+    for (int64_t k = b; k < b + U && k < blocks; ++k) {
+      const int64_t left = n - k * kStateBlock - kQuad * static_cast<int>(threadIdx.x % kWave);
+      f(IC<1>{}, k, left < 0 ? 0 : left > kQuad ? kQuad : static_cast<int>(left));
+    }
+  }
 }
 
-template <int KIND>
-__global__ __launch_bounds__(kBlock) void decode_kernel(const uint8_t* codes, const float* scales,
-                                                        int64_t n, float* x) {
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  for (int64_t b = static_cast<int64_t>(blockIdx.x) * kWaves + wave; b * kStateBlock < n;
-       b += static_cast<int64_t>(gridDim.x) * kWaves)
-    decode_block<KIND>(codes, scales, n, x, b, threadIdx.x % kWave);
+template <int U, int KIND>
+__global__ __launch_bounds__(kConvertWaves * kWave) void encode_kernel(const float* x, int64_t n,
+                                                                      uint8_t* codes,
+                                                                      float* scales) {
+  convert_all<U>(n, [&](auto u, int64_t b, int k) {
+    encode_blocks<decltype(u)::value, KIND>(x, codes, scales, b, threadIdx.x % kWave, k);
+  });
 }
 
-// A workgroup per kUnit values, up to what a launch counts (2^24 workgroups of
-// 256 lanes): 1.0e9 values to 8 bits 866 us, 5.8 TB/s, against 939 with eight
-// persistent workgroups per CU and more with fewer.
-unsigned convert_grid(int64_t n) {
-  const int64_t blocks = (n - 1) / kUnit + 1;
-  return static_cast<unsigned>(blocks < kMaxGroups ? blocks : kMaxGroups);
+template <int U, int KIND>
+__global__ __launch_bounds__(kConvertWaves * kWave) void decode_kernel(const uint8_t* codes,
+                                                                      const float* scales,
+                                                                      int64_t n, float* x) {
+  convert_all<U>(n, [&](auto u, int64_t b, int k) {
+    decode_blocks<decltype(u)::value, KIND>(codes, scales, x, b, threadIdx.x % kWave, k);
+  });
+}
+
+// Calls f(U, KIND, workgroups): for all blocks of n values at once, up to what
+// a launch counts.
+template <class F>
+void with_convert(int64_t n, int kind, F&& f) {
+  const auto go = [&](auto u, auto k) {
+    constexpr int64_t each = static_cast<int64_t>(decltype(u)::value) * kConvertWaves * kStateBlock;
+    constexpr int64_t most = kMaxGroups * kBlock / (kConvertWaves * kWave);
+    const int64_t groups = (n - 1) / each + 1;
+    f(u, k, dim3(static_cast<unsigned>(groups < most ? groups : most)));
+  };
+  if (n < kConvertFew)
+    kind == ZS_STATE8_M ? go(IC<1>{}, IC<ZS_STATE8_M>{}) : go(IC<1>{}, IC<ZS_STATE8_V>{});
+  else
+    kind == ZS_STATE8_M ? go(IC<2>{}, IC<ZS_STATE8_M>{}) : go(IC<2>{}, IC<ZS_STATE8_V>{});
 }
 
 }  // namespace
@@ -246,22 +293,21 @@ hipError_t launch_steps_advance(AwStepsDev* t, const double* sumsq, hipStream_t 
 
 hipError_t launch_state8_encode(const float* x, int64_t n, int kind, void* codes, float* scales,
                                 hipStream_t stream) {
-  const dim3 gd(convert_grid(n)), bd(kBlock);
-  if (kind == ZS_STATE8_M)
-    encode_kernel<ZS_STATE8_M><<<gd, bd, 0, stream>>>(x, n, static_cast<uint8_t*>(codes), scales);
-  else
-    encode_kernel<ZS_STATE8_V><<<gd, bd, 0, stream>>>(x, n, static_cast<uint8_t*>(codes), scales);
+  with_convert(n, kind, [&](auto u, auto k, dim3 grid) {
+    encode_kernel<decltype(u)::value, decltype(k)::value>
+        <<<grid, dim3(kConvertWaves * kWave), 0, stream>>>(x, n, static_cast<uint8_t*>(codes),
+                                                           scales);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_state8_decode(const void* codes, const float* scales, int64_t n, int kind,
                                 float* x, hipStream_t stream) {
-  const dim3 gd(convert_grid(n)), bd(kBlock);
-  const uint8_t* c = static_cast<const uint8_t*>(codes);
-  if (kind == ZS_STATE8_M)
-    decode_kernel<ZS_STATE8_M><<<gd, bd, 0, stream>>>(c, scales, n, x);
-  else
-    decode_kernel<ZS_STATE8_V><<<gd, bd, 0, stream>>>(c, scales, n, x);
+  with_convert(n, kind, [&](auto u, auto k, dim3 grid) {
+    decode_kernel<decltype(u)::value, decltype(k)::value>
+        <<<grid, dim3(kConvertWaves * kWave), 0, stream>>>(static_cast<const uint8_t*>(codes),
+                                                           scales, n, x);
+  });
   return hipGetLastError();
 }
 

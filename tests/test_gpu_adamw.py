@@ -429,7 +429,7 @@ def test_every_code_decodes_and_encodes(kind):
 
 
 @pytest.mark.parametrize("kind", ["m", "v"])
-@pytest.mark.parametrize("n", [1, 3, 255, 256, 257, 4097, 1_000_003])
+@pytest.mark.parametrize("n", [1, 3, 255, 256, 257, 4097, 1_000_003, 2_100_000])
 @pytest.mark.parametrize("shift", [0, 1])
 def test_convert(kind, n, shift):
     r = np.random.default_rng(n)

@@ -126,7 +126,7 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
     aligned = aligned && lo % size == 0;
     to.push_back({lo, lo + size * static_cast<uintptr_t>(n)});
   };
-  bool all_mean = npieces > 0;
+  bool all_mean = npieces > 0, on_lines = true;
   for (int32_t i = 0; i < npieces; ++i) {
     const zs_adamw_piece& q = pieces[i];
     if (q.len < 1 || q.len > kMaxLen || q.index < 0 || q.index > kMaxLen) return ZS_ERR_ARG;
@@ -145,6 +145,10 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
     span(writes, q.m, ssize, q.len);
     span(writes, q.v, ssize, q.len);
     if (param_dtype != 0) span(writes, q.param, 2, q.len);
+    for (const void* at : {static_cast<const void*>(q.w), static_cast<const void*>(q.m),
+                           static_cast<const void*>(q.v),
+                           static_cast<const void*>(param_dtype != 0 ? q.param : nullptr)})
+      on_lines = on_lines && reinterpret_cast<uintptr_t>(at) % 128 == 0;
     if (state_bits == 8) {
       if (!q.m_scale || !q.v_scale) return ZS_ERR_NULL;
       const int64_t nb = (q.len - 1) / ZS_STATE8_BLOCK + 1;
@@ -251,6 +255,8 @@ zs_status upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p, int32
   table->param_dtype = state_bits != 0 ? param_dtype : 0;
   table->state_bits = state_bits;
   table->has_mean = all_mean ? 1 : 0;
+  table->on_lines = on_lines ? 1 : 0;
+  table->reserved = 0;
   return ZS_OK;
 }
 
@@ -333,6 +339,7 @@ zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_steps* steps,
   L.pdt = t->param_dtype ? t->param_dtype : ZS_BF16;
   L.bits = t->state_bits;
   L.rounding = hp->rounding;
+  L.on_lines = t->on_lines != 0;
   L.stream = static_cast<hipStream_t>(stream);
   return from_hip(t->state_bits == 32 ? zs::launch_adamw32(L) : zs::launch_adamw8(L));
 }

@@ -73,6 +73,7 @@ struct AwLaunch {
   int64_t nchunks;
   int log_blocks;  // blocks of 256 elements per chunk, a power of two's exponent
   int gdt, pdt, bits, rounding;
+  bool on_lines;  // every tensor's arrays begin on a 128-byte line
   hipStream_t stream;
 };
 

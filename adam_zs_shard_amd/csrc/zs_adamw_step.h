@@ -172,9 +172,10 @@ __global__ __launch_bounds__(W * kWave) void adamw_kernel(AwArgs a) {
 // 15.6M elements and 8 ranks 105.6 us (four waves 107.6, sixteen 112); from
 // kManyRanks on four waves, two such: 30M elements and 16 ranks 273 us against
 // 292, 15M and 64 ranks 399 against 423.
-// 8-bit moments: eight waves, as many as fit (they compute more per byte): 2.57
-// ms (two 2.53, four 2.56), buffers that begin inside a line 2.80 (3.24, 2.99);
-// 15.6M elements and 8 ranks 85.0 us (four 88.3, two 92.2).
+// 8-bit moments, as many waves as fit (they compute more per byte): with one
+// gradient two waves where all arrays begin on a line, 2.53 ms (four 2.56,
+// eight 2.57-2.61), else eight, 2.80 (two 3.24, four 2.99); with several
+// eight, 15.6M elements and 8 ranks 85.0 us (four 88.3, two 92.2).
 // A small table's chunks have four blocks, which is four waves at most.
 constexpr unsigned kReserveOne = 160 * 1024 / 16 - 64, kReserveRanks = 160 * 1024 / 2 - 64;
 constexpr int kManyRanks = 16;
@@ -202,7 +203,10 @@ void launch_step(const AwLaunch& L) {
         else
           go(IC<8>{}, IC<0>{}, lds);
       } else if (L.a.p == 1) {
-        small ? go(IC<4>{}, IC<1>{}, 0) : go(IC<8>{}, IC<1>{}, 0);
+        if (L.on_lines)
+          go(IC<2>{}, IC<1>{}, 0);
+        else
+          small ? go(IC<4>{}, IC<1>{}, 0) : go(IC<8>{}, IC<1>{}, 0);
       } else {
         small ? go(IC<4>{}, IC<0>{}, 0) : go(IC<8>{}, IC<0>{}, 0);
       }

@@ -38,7 +38,8 @@ class zs_adamw_piece(C.Structure):
 class zs_adamw_table(C.Structure):
     _fields_ = [("workspace", C.c_void_p), ("nchunks", C.c_int64), ("chunk_elems", C.c_int64),
                 ("npieces", C.c_int32), ("p", C.c_int32), ("grad_dtype", C.c_int32),
-                ("param_dtype", C.c_int32), ("state_bits", C.c_int32), ("has_mean", C.c_int32)]
+                ("param_dtype", C.c_int32), ("state_bits", C.c_int32), ("has_mean", C.c_int32),
+                ("on_lines", C.c_int32), ("reserved", C.c_int32)]
 
 
 class zs_adamw_hparams(C.Structure):

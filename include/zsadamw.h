@@ -91,6 +91,8 @@ typedef struct {
   int32_t param_dtype;  /* zs_dtype, or 0: no working copy */
   int32_t state_bits;   /* 32, 8, or 0: gradients only */
   int32_t has_mean;     /* every piece has g_mean */
+  int32_t on_lines;     /* every w, m, v and param begins on a 128-byte line */
+  int32_t reserved;
 } zs_adamw_table;
 
 /* Device bytes that zs_adamw_upload needs for tensors of lens[0..npieces)

@@ -108,7 +108,7 @@ def test_upload_refuses_arguments():
 
 
 def _table(**over):
-    t = a.zs_adamw_table(WS, 4, 8192, 2, 2, z.ZS_BF16, z.ZS_BF16, 32, 1)
+    t = a.zs_adamw_table(WS, 4, 8192, 2, 2, z.ZS_BF16, z.ZS_BF16, 32, 1, 0, 0)
     for k, x in over.items():
         setattr(t, k, x)
     return t

@@ -50,8 +50,10 @@ class Buffers:
     def __init__(self, lens, dtype, shift):
         self.lens, self.dtype = lens, dtype
         size = torch.empty(0, dtype=dtype).element_size()
-        self.offs, at = [], shift + GAP
+        self.offs, at = [], GAP
         for n in lens:
+            # shift None: every tensor on a 128-byte line
+            at = -(-at // 256) * 256 if shift is None else at + shift * (not self.offs)
             self.offs.append(at)
             at += n + GAP
         raw = {4: torch.int32, 2: torch.int16, 1: torch.uint8}[size]
@@ -212,11 +214,20 @@ def test_step_of_odd_tensors(bits, grad, param, p, shift):
 
 
 @pytest.mark.parametrize("bits,rounding", [(32, "nearest"), (8, "nearest"), (8, "stochastic")])
-@pytest.mark.parametrize("p", [1, 4])
-def test_step_of_large_tensors(bits, rounding, p):
+@pytest.mark.parametrize("p,shift", [(1, 0), (1, None), (4, 0), (4, None), (17, 1)])
+def test_step_of_large_tensors(bits, rounding, p, shift):
     # enough for the larger workgroups, pieces that end inside one
-    M = Model([3_000_001, 513, 1_300_000, 77], p, "bf16", "bf16", bits, seed=20)
+    M = Model([3_000_001, 513, 1_300_000, 77], p, "bf16", "bf16", bits, shift, seed=20)
+    assert M.table.on_lines == (shift is None) and M.table.chunk_elems > 2048
     M.step_and_check(17, rounding=rounding, seed=(7 << 32) + 5)
+
+
+@pytest.mark.parametrize("bits,rounding", [(32, "nearest"), (8, "nearest"), (8, "stochastic")])
+@pytest.mark.parametrize("p", [1, 3])
+def test_step_of_odd_tensors_on_lines(bits, rounding, p):
+    M = Model(ODD, p, "f16", "bf16", bits, None, seed=21)
+    assert M.table.on_lines == 1
+    M.step_and_check(4, rounding=rounding, seed=5)
 
 
 @pytest.mark.parametrize("grad", ["f16", "f32"])

@@ -16,7 +16,11 @@ namespace {
 constexpr int64_t kMaxLen = int64_t{1} << 60;
 using zs::kMaxGroups;
 
-// Elements per entry of the launch table, in units of one workgroup.
+// Elements per entry of the launch table: 8192, or, in tables of fewer than 512
+// such, 1024: short tensors then launch no idle waves (50,000 elements in 16
+// tensors: 2.9 us either way on the GPU), and the norm's workgroups find a
+// unit each.  1.0e9 elements with entries of 2048 / 4096 / 8192 / 32,768: 5.06
+// / 5.05 / 5.03 / 5.04 ms.
 constexpr int kUnitsLarge = 3, kUnitsSmall = 0;
 constexpr int64_t kChunkLarge = int64_t{zs::kUnit} << kUnitsLarge;
 constexpr int64_t kChunkSmall = int64_t{zs::kUnit} << kUnitsSmall;

@@ -37,7 +37,8 @@ __device__ __forceinline__ void sumsq_blocks(const Chunk& ch, const uint64_t* gp
 #pragma unroll
     for (int u = 0; u < U; ++u) widen4<GDT>(q[u], g[u]);
   } else {
-    mean_ranks<U, GDT>(rank_ptrs(gptrs, ch.piece, p), p, PF, ch.start + e0, lane, n, g);
+    static_assert(U == 1, "one block of several ranks at a time");
+    mean_ranks<GDT>(rank_ptrs(gptrs, ch.piece, p), p, PF, ch.start + e0, lane, n, g[0]);
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {

@@ -9,119 +9,107 @@
 namespace zs {
 namespace {
 
-// U blocks of 256 elements by one wave, from block b of the chunk on.  n < 0:
-// whole blocks; else (U = 1) the lane's n (0..4) elements of a tensor's last
-// block.
-template <int U, int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
-__device__ __forceinline__ void step_blocks(const AwArgs& a, const AwConsts& c, const Chunk& ch,
-                                            float GS, float LR,
-                                            float LD, int b, uint32_t lane, int n) {
-  const int64_t e0 = static_cast<int64_t>(b) * kStateBlock;
-  float g[U][kQuad], w[U][kQuad], m[U][kQuad], v[U][kQuad];
-  Raw4<kF32> wq[U], mq[U], vq[U];
-  uint32_t mc[U], vc[U];
-  float ms[U], vs[U];
-  Raw4<GDT> gq[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t e = e0 + u * kStateBlock;
-    if constexpr (ONE) {
-      // a single gradient goes through plain loads beside 32-bit moments (1.0e9
-      // elements 4.79 -> 4.63 ms), non-temporal ones beside 8-bit moments
-      // (equal) and from several ranks (15.6M elements, 8 ranks 107.5 us, 110.2
-      // with plain ones)
-      const char* gb = ch.g + e * kSize<GDT>;
-      gq[u] = n < 0 ? ld_raw4<GDT, BITS == 8>(gb, lane) : ld_raw4<GDT>(gb, lane, n);
-    }
-    wq[u] = n < 0 ? ld_raw4<kF32>(ch.w + e, lane) : ld_raw4<kF32>(ch.w + e, lane, n);
-    if constexpr (BITS == 32) {
-      const float* mb = reinterpret_cast<const float*>(ch.m) + e;
-      const float* vb = reinterpret_cast<const float*>(ch.v) + e;
-      mq[u] = n < 0 ? ld_raw4<kF32>(mb, lane) : ld_raw4<kF32>(mb, lane, n);
-      vq[u] = n < 0 ? ld_raw4<kF32>(vb, lane) : ld_raw4<kF32>(vb, lane, n);
-    } else {
-      mc[u] = n < 0 ? ld_codes(ch.m + e, lane) : ld_codes(ch.m + e, lane, n);
-      vc[u] = n < 0 ? ld_codes(ch.v + e, lane) : ld_codes(ch.v + e, lane, n);
-      ms[u] = ch.m_scale[b + u];
-      vs[u] = ch.v_scale[b + u];
-    }
-  }
+// One block of 256 elements by one wave.  n < 0: a whole block; else the lane's
+// n (0..4) elements of a tensor's last block.
+template <int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
+__device__ __forceinline__ void step_block(const AwArgs& a, const AwConsts& c, const Chunk& ch,
+                                           float GS, float LR, float LD, int b, uint32_t lane,
+                                           int n) {
+  const int64_t e = static_cast<int64_t>(b) * kStateBlock;
+  float g[kQuad], w[kQuad], m[kQuad], v[kQuad];
+  Raw4<kF32> mq, vq;
+  uint32_t mc, vc;
+  float ms, vs;
+  Raw4<GDT> gq;
   if constexpr (ONE) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) widen4<GDT>(gq[u], g[u]);
+    // a single gradient goes through plain loads beside 32-bit moments (1.0e9
+    // elements 4.79 -> 4.63 ms), non-temporal ones beside 8-bit moments
+    // (equal) and from several ranks (15.6M elements, 8 ranks 107.5 us, 110.2
+    // with plain ones)
+    const char* gb = ch.g + e * kSize<GDT>;
+    gq = n < 0 ? ld_raw4<GDT, BITS == 8>(gb, lane) : ld_raw4<GDT>(gb, lane, n);
+  }
+  const Raw4<kF32> wq = n < 0 ? ld_raw4<kF32>(ch.w + e, lane) : ld_raw4<kF32>(ch.w + e, lane, n);
+  if constexpr (BITS == 32) {
+    const float* mb = reinterpret_cast<const float*>(ch.m) + e;
+    const float* vb = reinterpret_cast<const float*>(ch.v) + e;
+    mq = n < 0 ? ld_raw4<kF32>(mb, lane) : ld_raw4<kF32>(mb, lane, n);
+    vq = n < 0 ? ld_raw4<kF32>(vb, lane) : ld_raw4<kF32>(vb, lane, n);
   } else {
-    mean_ranks<U, GDT>(rank_ptrs(a.gptrs, ch.piece, a.p), a.p, a.PF, ch.start + e0, lane, n, g);
+    mc = n < 0 ? ld_codes(ch.m + e, lane) : ld_codes(ch.m + e, lane, n);
+    vc = n < 0 ? ld_codes(ch.v + e, lane) : ld_codes(ch.v + e, lane, n);
+    ms = ch.m_scale[b];
+    vs = ch.v_scale[b];
+  }
+  if constexpr (ONE)
+    widen4<GDT>(gq, g);
+  else
+    mean_ranks<GDT>(rank_ptrs(a.gptrs, ch.piece, a.p), a.p, a.PF, ch.start + e, lane, n, g);
+  widen4<kF32>(wq, w);
+  if constexpr (BITS == 32) {
+    widen4<kF32>(mq, m);
+    widen4<kF32>(vq, v);
+  } else {
+    decode4<ZS_STATE8_M>(mc, ms, m);
+    decode4<ZS_STATE8_V>(vc, vs, v);
   }
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int64_t e = e0 + u * kStateBlock;
-    widen4<kF32>(wq[u], w[u]);
+  for (int j = 0; j < kQuad; ++j) {
+    moments1(c, g[j] * GS, m[j], v[j]);
+    float x;
     if constexpr (BITS == 32) {
-      widen4<kF32>(mq[u], m[u]);
-      widen4<kF32>(vq[u], v[u]);
+      x = (m[j] / c.A1) / (__builtin_sqrtf(v[j] / c.A2) + c.EPS);
     } else {
-      decode4<ZS_STATE8_M>(mc[u], ms[u], m[u]);
-      decode4<ZS_STATE8_V>(vc[u], vs[u], v[u]);
+      // the hardware's root and reciprocal: the 8-bit step is as much bound by
+      // its arithmetic as by HBM, and moments that are held to 2^-4 need no
+      // correctly rounded quotient
+      x = m[j] * __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[j]) * c.R2 + c.EPS);
     }
+    w[j] = w[j] - (LR * x + LD * w[j]);
+  }
+  if (n < 0) {
+    st_quad32(ch.w + e, lane, w);
+    if (ch.param) st_quad16<PDT>(ch.param + e, lane, w);
+  } else {
+    st_quad32(ch.w + e, lane, n, w);
+    if (ch.param) st_quad16<PDT>(ch.param + e, lane, n, w);
+  }
+  if constexpr (BITS == 32) {
+    float* mb = reinterpret_cast<float*>(ch.m) + e;
+    float* vb = reinterpret_cast<float*>(ch.v) + e;
+    if (n < 0) {
+      st_quad32(mb, lane, m);
+      st_quad32(vb, lane, v);
+    } else {
+      st_quad32(mb, lane, n, m);
+      st_quad32(vb, lane, n, v);
+    }
+  } else {
+    // elements behind the tensor's end are zeros here: they raise no maximum
+    // (v is never negative, so its bits are its magnitude's)
+    uint32_t mm = 0, vm = 0;
 #pragma unroll
     for (int j = 0; j < kQuad; ++j) {
-      moments1(c, g[u][j] * GS, m[u][j], v[u][j]);
-      float x;
-      if constexpr (BITS == 32) {
-        x = (m[u][j] / c.A1) / (__builtin_sqrtf(v[u][j] / c.A2) + c.EPS);
-      } else {
-        // the hardware's root and reciprocal: the 8-bit step is as much bound
-        // by its arithmetic as by HBM, and moments that are held to 2^-4 need
-        // no correctly rounded quotient
-        x = m[u][j] *
-            __builtin_amdgcn_rcpf(__builtin_amdgcn_sqrtf(v[u][j]) * c.R2 + c.EPS);
-      }
-      w[u][j] = w[u][j] - (LR * x + LD * w[u][j]);
+      mm = mag_bits(m[j]) > mm ? mag_bits(m[j]) : mm;
+      vm = __float_as_uint(v[j]) > vm ? __float_as_uint(v[j]) : vm;
     }
+    BlockScale sm, sv;
+    float mine;
+    block_scales(wave_max(mm), wave_max(vm), lane, sm, sv, mine);
+    uint32_t word[kQuad] = {0u, 0u, 0u, 0u};
+    if constexpr (RANDOM)
+      philox(static_cast<uint64_t>(ch.index + e + kQuad * lane), static_cast<uint64_t>(c.step),
+             a.seed, word);
+    const uint32_t cm = encode4<ZS_STATE8_M, RANDOM>(m, sm, word);
+    const uint32_t cv = encode4<ZS_STATE8_V, RANDOM>(v, sv, word);
     if (n < 0) {
-      st_quad32(ch.w + e, lane, w[u]);
-      if (ch.param) st_quad16<PDT>(ch.param + e, lane, w[u]);
+      st_codes(ch.m + e, lane, cm);
+      st_codes(ch.v + e, lane, cv);
     } else {
-      st_quad32(ch.w + e, lane, n, w[u]);
-      if (ch.param) st_quad16<PDT>(ch.param + e, lane, n, w[u]);
+      st_codes(ch.m + e, lane, n, cm);
+      st_codes(ch.v + e, lane, n, cv);
     }
-    if constexpr (BITS == 32) {
-      float* mb = reinterpret_cast<float*>(ch.m) + e;
-      float* vb = reinterpret_cast<float*>(ch.v) + e;
-      if (n < 0) {
-        st_quad32(mb, lane, m[u]);
-        st_quad32(vb, lane, v[u]);
-      } else {
-        st_quad32(mb, lane, n, m[u]);
-        st_quad32(vb, lane, n, v[u]);
-      }
-    } else {
-      // elements behind the tensor's end are zeros here: they raise no maximum
-      // (v is never negative, so its bits are its magnitude's)
-      uint32_t mm = 0, vm = 0;
-#pragma unroll
-      for (int j = 0; j < kQuad; ++j) {
-        mm = mag_bits(m[u][j]) > mm ? mag_bits(m[u][j]) : mm;
-        vm = __float_as_uint(v[u][j]) > vm ? __float_as_uint(v[u][j]) : vm;
-      }
-      BlockScale sm, sv;
-      float mine;
-      block_scales(wave_max(mm), wave_max(vm), lane, sm, sv, mine);
-      uint32_t word[kQuad] = {0u, 0u, 0u, 0u};
-      if constexpr (RANDOM)
-        philox(static_cast<uint64_t>(ch.index + e + kQuad * lane),
-               static_cast<uint64_t>(c.step), a.seed, word);
-      const uint32_t cm = encode4<ZS_STATE8_M, RANDOM>(m[u], sm, word);
-      const uint32_t cv = encode4<ZS_STATE8_V, RANDOM>(v[u], sv, word);
-      if (n < 0) {
-        st_codes(ch.m + e, lane, cm);
-        st_codes(ch.v + e, lane, cv);
-      } else {
-        st_codes(ch.m + e, lane, n, cm);
-        st_codes(ch.v + e, lane, n, cv);
-      }
-      if (lane % (kWave / 2) == 0) (lane == 0 ? ch.m_scale : ch.v_scale)[b + u] = mine;
-    }
+    if (lane % (kWave / 2) == 0) (lane == 0 ? ch.m_scale : ch.v_scale)[b] = mine;
   }
 }
 
@@ -154,11 +142,11 @@ __global__ __launch_bounds__(W * kWave) void adamw_kernel(AwArgs a) {
   const float LD = static_cast<float>(lr * ch.decay);
   const uint32_t lane = threadIdx.x % kWave;
   if (left >= kStateBlock) {
-    step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, c, ch, s.GS, LR, LD, b, lane, -1);
+    step_block<GDT, PDT, BITS, RANDOM, ONE>(a, c, ch, s.GS, LR, LD, b, lane, -1);
   } else {
     int n = left - kQuad * static_cast<int>(lane);
     n = n < 0 ? 0 : n > kQuad ? kQuad : n;
-    step_blocks<1, GDT, PDT, BITS, RANDOM, ONE>(a, c, ch, s.GS, LR, LD, b, lane, n);
+    step_block<GDT, PDT, BITS, RANDOM, ONE>(a, c, ch, s.GS, LR, LD, b, lane, n);
   }
 }
 

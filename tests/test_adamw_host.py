@@ -35,6 +35,8 @@ def test_workspace_bytes():
     assert need([5000, 7], 8) - need([5000, 7], 1) >= 0
     assert need([2048 * 100], 1) >= 100 * 128
     assert need([10**9], 1) < 10**9 // 8192 * 128 + 4096 * 16
+    # short tensors: entries of their own size
+    assert need([1000] * 10_000, 1) < 10_000 * (2 * 128 + 8) + 4096 * 16
     for bad in ([0], [-1], [1 << 61], [1 << 59, 1 << 59, 1 << 59]):
         assert need(bad, 1) == 0
     assert need([5], 0) == 0 and need([5], z.ZS_MAX_P + 1) == 0

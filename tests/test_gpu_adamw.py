@@ -623,3 +623,110 @@ def test_captured_steps_follow_a_step_table(bits, rounding):
         for x, y in zip(M.all(), E.all()):
             assert np.array_equal(bits_of(x.flat), bits_of(y.flat)), f"replay {i}"
     assert done == len(lrs)
+
+
+# ---- calls that nothing above makes ---------------------------------------------------
+def test_most_ranks_and_shared_gradients():
+    """ZS_MAX_P ranks; then ranks and tensors that all read one buffer."""
+    M = Model([700, 1], z.ZS_MAX_P, "bf16", "bf16", 8, seed=90)
+    M.step_and_check(2, bounds=False)
+    M = Model([3000, 3000], 3, "f32", "f16", 32, seed=91)
+    ps = M.pieces()
+    one = M.g[0][0]
+    for q in ps:
+        q["grads"] = [one] * 3
+    M.table = a.zs_adamw_upload(ps, 3, "f32", "f16", 32, M.ws, M.ws.numel())
+    for b in M.g:
+        for i in range(2):
+            b[i].copy_(one)
+    M.step_and_check(2)
+    out = torch.zeros((), dtype=torch.float64, device=DEV)
+    a.zs_grad_sumsq_multi(M.table, out)
+    x = ref.mean32([one.cpu().numpy()] * 3).astype(np.float64)
+    assert abs(out.item() - 2 * np.dot(x, x)) <= 6000 * 2.0 ** -53 * out.item()
+
+
+def test_nonfinite_gradients_stay_in_their_elements():
+    """32-bit moments: IEEE rules element by element."""
+    M = Model([1000], 1, "f32", "bf16", 32, seed=92)
+    g = M.g[0][0]
+    g[5], g[6], g[7], g[999] = float("inf"), float("-inf"), float("nan"), 3e38
+    M.step_and_check(2, bounds=False)
+    bad = ~np.isfinite(M.w[0].cpu().numpy())
+    assert bad[[5, 6, 7]].all() and bad.sum() == 3
+
+
+def test_values_outside_the_copy_and_zero_moments():
+    M = Model([600], 1, "bf16", "f16", 32, seed=93, states=False)
+    M.w[0][:3] = torch.tensor([1e6, -1e6, 1e-9], device=DEV)
+    M.g[0][0].zero_()
+    M.step_and_check(1, bounds=False)  # 0 / (0 + eps) moves nothing; the copy overflows and underflows
+    assert M.pb[0][:2].isinf().all() and M.pb[0][2] == 0
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_first_step_from_zero_states(bits):
+    """Codes and scales all zero are the zero state; step 1 moves by lr where the
+    gradient is far above eps."""
+    M = Model([5000, 10], 1, "bf16", "bf16", bits, seed=94, states=False, gscale=1.0)
+    M.decay = [0.0, 0.0]
+    M.table = M.upload()
+    w0, g = M.w[0].clone(), M.g[0][0].float()
+    M.step_and_check(1)
+    moved = (M.w[0] - w0)[g.abs() > 1e-2]
+    # lr * (1 +- 8 half steps), and w's own rounding (w < 1/8: half a step is 2^-28)
+    assert float((moved.abs() - LR).abs().max()) <= LR * 8 * ref.U + 2.0 ** -27
+
+
+def test_current_stream_is_taken():
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        assert z._stream(None) == s.cuda_stream
+    assert z._stream(None) == torch.cuda.current_stream().cuda_stream
+    assert z._stream(s) == s.cuda_stream and z._stream(5) == 5
+
+
+def test_two_graphs_replayed_on_two_streams():
+    """Two captured loops with tables of their own, replayed at once."""
+    sets = []
+    for i in range(2):
+        M, E = (Model([100_003, 700], 1, "bf16", "bf16", 8, seed=95 + i) for _ in range(2))
+        out = torch.zeros((), dtype=torch.float64, device=DEV)
+        hp = a.hparams(LR, B1, B2, EPS, 3, max_norm=1.0, rounding="stochastic", seed=i)
+        graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            with torch.cuda.graph(graph):
+                a.zs_grad_sumsq_multi(M.table, out)
+                a.zs_adamw_step_multi(M.table, hp, out)
+        sets.append((M, E, out, hp, graph, s))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for M, E, out, hp, graph, s in sets:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for M, E, out, hp, graph, s in sets:
+        one = torch.zeros_like(out)
+        for _ in range(3):
+            a.zs_grad_sumsq_multi(E.table, one)
+            a.zs_adamw_step_multi(E.table, hp, one)
+        assert one.item() == out.item()
+        for x, y in zip(M.all(), E.all()):
+            assert np.array_equal(bits_of(x.flat), bits_of(y.flat))
+
+
+def test_moments_move_between_the_forms():
+    """32-bit moments encoded, stepped in 8 bits, decoded and stepped in 32."""
+    n = 5000
+    A, B = Model([n], 1, "bf16", "bf16", 32, seed=97), Model([n], 1, "bf16", "bf16", 8, seed=97)
+    a.zs_state8_encode(A.m[0], n, "m", B.m[0], B.ms[0])
+    a.zs_state8_encode(A.v[0], n, "v", B.v[0], B.vs[0])
+    B.w[0].copy_(A.w[0])
+    B.step_and_check(7, rounding="stochastic", seed=1)
+    a.zs_state8_decode(B.m[0], B.ms[0], n, "m", A.m[0])
+    a.zs_state8_decode(B.v[0], B.vs[0], n, "v", A.v[0])
+    A.w[0].copy_(B.w[0])
+    A.step_and_check(8)
+    for b in A.all() + B.all():
+        b.check("buffer")

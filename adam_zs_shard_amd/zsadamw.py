@@ -92,7 +92,7 @@ def lib():
 
 
 def _named(x, names) -> int:
-    return names[x] if isinstance(x, str) else int(x or 0)
+    return names[x] if x.__class__ is str else int(x or 0)
 
 
 def hparams(lr, beta1, beta2, eps, step, *, grad_scale=1.0, max_norm=0.0, rounding="nearest",

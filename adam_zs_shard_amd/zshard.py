@@ -194,18 +194,28 @@ def _dtype_of(x, given) -> int:
     raise ValueError(f"16-bit tensor expected, got {x.dtype}")
 
 
-def _stream(stream):
-    if stream is None:
+_raw_stream = None  # (handle of a device's current stream, current device), once torch has a GPU
+
+
+def _current_stream():
+    """The current stream's handle.  torch.cuda.current_stream() builds a Stream
+    object around it, 3 us of the 8 that a call took; this takes 0.2."""
+    global _raw_stream
+    if _raw_stream is None:
         import torch
 
-        # the current stream's handle without a Stream object around it: 0.3
-        # instead of 3.5 us, of the 8 us that a call took
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None and torch.cuda.is_initialized():
-            return raw(torch.cuda.current_device())
-        if torch.cuda.is_available():
+        if not torch.cuda.is_available():
+            return None
+        if not torch.cuda.is_initialized() or not hasattr(torch._C, "_cuda_getCurrentRawStream"):
             return torch.cuda.current_stream().cuda_stream
-        return None
+        _raw_stream = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    handle, device = _raw_stream
+    return handle(device())
+
+
+def _stream(stream):
+    if stream is None:
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

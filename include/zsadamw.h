@@ -20,7 +20,7 @@
  * for bit.  With 8-bit states lr_i*u is f32(lr_i/(1-beta1^t)) * (m' /
  * (sqrt(v') * f32(1/sqrt(1-beta2^t)) + eps)), from the moments before they
  * are rounded, where the root and the reciprocal are the hardware's, within
- * 1 ulp each, and a v' or a divisor below 2^-126 counts as 0.
+ * 1 ulp each, and a v' or a divisor below 2^-126 may count as 0.
  * gs = f32(grad_scale * coef), coef = min(1, max_norm / (sqrt(sumsq) *
  * |grad_scale| + 1e-6)) in double where a norm is given, else 1.
  *
@@ -29,8 +29,9 @@
  * per moment, and a value is its code times the scale.  m: OCP e4m3 codes,
  * scale = max|m'| * f32(1/448).  v: OCP e5m2 codes, scale = max v' *
  * f32(1/57344).  Codes are those of x * f32(top / max) cut to [-top, top]:
- * m is off by at most 1/16 and sqrt(v) by about as much, whatever a value's
- * size within 2^14 (m) or 2^29 (v) of its block's largest.  A positive v
+ * m is off by at most 1/16 and sqrt(v) by about as much (twice that with
+ * random rounding), whatever a value's size within 2^14 (m) or 2^29 (v) of its
+ * block's largest.  A positive v
  * never gets code 0, since the update divides by its root.  A block whose
  * largest value is below 2^-110 is held as zeros; one that holds an infinity
  * or NaN gets a NaN scale and codes 0, so that all of it reads as NaN (see
@@ -100,17 +101,22 @@ typedef struct {
 size_t zs_adamw_workspace_bytes(const int64_t* lens, int32_t npieces, int32_t p);
 
 /* Writes the launch table of the tensors into the caller's device workspace
- * (256-byte aligned) with one copy on `stream`, and waits for it.  Call once
- * per plan: the table stays valid while the memory that it names does.  One
- * table may be used by one stream at a time (zs_grad_sumsq_multi keeps its
- * partial sums in the workspace).
+ * (256-byte aligned) with one copy on `stream`, and waits for it (call it
+ * before capture).  Call once per plan: the table stays valid while the memory
+ * that it names does.  One table may be used by one stream at a time
+ * (zs_grad_sumsq_multi keeps its partial sums in the workspace).
+ * Tensors may begin anywhere; steps are fastest where the arrays of a tensor
+ * all begin on a 128-byte line or the same number of elements past one.  With
+ * 8-bit states only the caller can see to that (blocks are counted from the
+ * tensor's first element): 10% on 1.0e9 elements.
  *  state_bits: 32 or 8; 0 for a table of gradients only (zs_grad_sumsq_multi),
  *     whose w, m, v, param and scales are not looked at.
  *  param_dtype: ZS_F16 or ZS_BF16; 0 for no working copy.
  * Errors: ZS_ERR_NULL, ZS_ERR_ARG (p outside 1..ZS_MAX_P, state_bits, a len,
  * index, weight_decay or lr_scale out of range, an address that is no multiple
- * of its element size), ZS_ERR_RANGE, ZS_ERR_DTYPE, ZS_ERR_CAPACITY (the
- * workspace is too small or misaligned), ZS_ERR_ALIAS (what one tensor has
+ * of its element size), ZS_ERR_RANGE (more than one launch holds: about 1.7e10
+ * elements or, in short tensors, 1.6e7 of them), ZS_ERR_DTYPE, ZS_ERR_CAPACITY
+ * (the workspace is too small or misaligned), ZS_ERR_ALIAS (what one tensor has
  * written overlaps what any tensor has written or read, or the workspace),
  * ZS_ERR_HIP, ZS_ERR_RESOURCE. */
 zs_status zs_adamw_upload(const zs_adamw_piece* pieces, int32_t npieces, int32_t p,
@@ -145,6 +151,7 @@ typedef struct {
  * grad_scale (zs_grad_sumsq_multi, summed over the shards), or NULL.
  * Bytes per element: p gradients + 4 + 4 (w) + 2 (param) + 16 (32-bit
  * states) or 4.0625 (8-bit).  Elements beyond a tensor's len are not touched.
+ * A table of no tensors returns ZS_OK without launching.
  * Errors: ZS_ERR_NULL, ZS_ERR_ARG, ZS_ERR_DTYPE, ZS_ERR_HIP. */
 zs_status zs_adamw_step_multi(const zs_adamw_table* table, const zs_adamw_hparams* hp,
                               const double* sumsq, void* stream);

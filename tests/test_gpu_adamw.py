@@ -542,8 +542,9 @@ def test_two_streams_at_once():
 
 @pytest.mark.parametrize("bits", [32, 8])
 def test_offsets_beyond_32_bits(bits):
-    """One tensor of 1.1e9 elements: its first and last blocks."""
-    n = 1_100_000_123
+    """One tensor of over 2^30 (32-bit moments) or 2^31 elements: blocks at its
+    start, in its middle and at its end."""
+    n = 1_100_000_123 if bits == 32 else 2_300_000_123
     gen = torch.Generator(device=DEV)
     gen.manual_seed(2)
     g = torch.randn(n, generator=gen, device=DEV, dtype=torch.bfloat16).mul_(1e-3)

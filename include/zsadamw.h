@@ -78,7 +78,8 @@ typedef struct {
   const void* const* grads; /* host array of p device pointers, rank order */
   double weight_decay;      /* finite, >= 0 */
   double lr_scale;          /* finite */
-  int64_t index;            /* >= 0: index of element 0 for ZS_ROUND_STOCHASTIC, e.g. in the whole model */
+  int64_t index;            /* >= 0: index of element 0 for ZS_ROUND_STOCHASTIC, e.g. in the whole model
+                             * (elements of equal index share their random bits) */
 } zs_adamw_piece;
 
 /* Host-side handle of an uploaded table. */

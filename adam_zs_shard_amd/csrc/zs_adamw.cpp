@@ -30,6 +30,10 @@ int64_t chunk_rule(int64_t total, int32_t npieces) {
   return total / kChunkLarge >= std::max(512, npieces) ? kChunkLarge : kChunkSmall;
 }
 int units_of(int64_t chunk) { return chunk == kChunkLarge ? kUnitsLarge : kUnitsSmall; }
+// Blocks of 256 elements per entry, a power of two's exponent.
+int log_blocks_of(int64_t chunk) {
+  return units_of(chunk) + zs::log2_of(zs::kUnit / zs::kStateBlock);
+}
 
 // Where the workspace's parts lie: the entries, the rank pointers, the norm's
 // count of arrivals and its partial sums (which alone are not uploaded).
@@ -336,7 +340,7 @@ zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_steps* steps,
   L.a.seed = hp->seed;
   L.a.p = t->p;
   L.a.skip_nonfinite = hp->skip_nonfinite;
-  L.log_blocks = units_of(t->chunk_elems) + zs::log2_of(zs::kUnit / zs::kStateBlock);
+  L.log_blocks = log_blocks_of(t->chunk_elems);
   L.a.PF = static_cast<float>(static_cast<double>(t->p));
   L.a.c = make_consts(*hp);
   L.nchunks = t->nchunks;
@@ -479,7 +483,7 @@ zs_status zs_grad_sumsq_multi(const zs_adamw_table* t, int32_t store_mean, int32
     L.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
     L.gptrs = reinterpret_cast<const uint64_t*>(base + lay.gptrs);
     L.nchunks = t->nchunks;
-    L.units = units_of(t->chunk_elems);
+    L.log_blocks = log_blocks_of(t->chunk_elems);
     L.p = t->p;
     L.gdt = t->grad_dtype;
     L.store = store_mean != 0;

@@ -81,7 +81,7 @@ struct SumsqLaunch {
   const AwChunk* chunks;
   const uint64_t* gptrs;
   int64_t nchunks;
-  int units;  // per chunk, a power of two's exponent
+  int log_blocks;  // as in AwLaunch
   int p, gdt;
   bool store, accumulate;
   double* partial;         // kSumsqBlocks doubles

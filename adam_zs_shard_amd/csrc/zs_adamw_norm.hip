@@ -58,15 +58,14 @@ __device__ __forceinline__ void sumsq_blocks(const Chunk& ch, const uint64_t* gp
 
 // Joining the workgroups' sums.  JOIN: the last workgroup to arrive adds them
 // up, in their order whoever it is, and makes the count ready for the next
-// launch.  That saves a launch (6.9 -> 4.6 us of the host's time), but each
-// arrival writes back and invalidates its L2: with 1024 workgroups it cost 40
-// us (15.6M elements, 8 ranks: 62 -> 105 us), so only launches of at most
-// kJoinMost workgroups do it, and tables of so few units that as many can
-// read them as fast (500,000 elements 4.8 us on the GPU, 5.2 with a workgroup
-// per unit and a second launch; with twice the units 7.7 and 5.6); the others
-// join in a second launch.
-constexpr int kJoinMost = 64;
-constexpr int64_t kJoinUnits = 8 * kJoinMost;  // times ranks
+// launch.  That saves a launch (3 us of the host's time), but each arrival
+// writes back and invalidates its L2: with 1024 workgroups it cost 40 us (15.6M
+// elements, 8 ranks: 62 -> 105 us).  So at most kJoinMost workgroups do it: of
+// kJoinWaves waves each for one rank's sums of up to kJoinTurns turns of theirs
+// (1.0e6 elements: 5.2 us on the GPU and 4.6 on the host, against 5.0 and 7.6
+// in two launches; two more turns 8.0 us on the GPU; 50,000 elements 4.3, with
+// sixteen waves 5.2), of four waves for several ranks' sums of one turn.
+constexpr int kJoinMost = 64, kJoinWaves = 8, kJoinTurns = 2;
 
 // One rank: four blocks per wave and turn, so that as many bytes are in
 // flight, four workgroups per CU (1.0e9 bf16 elements 299 us, 6.7 TB/s; two,
@@ -77,18 +76,21 @@ constexpr int64_t kJoinUnits = 8 * kJoinMost;  // times ranks
 constexpr int kLogOne = 2;
 constexpr int kLoadsOne = 1 << kLogOne;
 constexpr int kGroupsOne = 4, kGroupsRanks = 3;
-template <int U, int GDT, bool STORE, bool ONE, bool JOIN>
-__global__ __launch_bounds__(kBlock) void sumsq_kernel(const AwChunk* chunks,
-                                                       const uint64_t* gptrs, int64_t nunits,
-                                                       int units, int p, float PF, double* partial,
-                                                       unsigned int* arrived, int accumulate,
-                                                       double* out) {
+
+// A unit is the U blocks that a wave of W takes at a turn; a chunk has 2^shift.
+template <int W, int U, int GDT, bool STORE, bool ONE, bool JOIN>
+__global__ __launch_bounds__(W * kWave) void sumsq_kernel(const AwChunk* chunks,
+                                                          const uint64_t* gptrs, int64_t nunits,
+                                                          int shift, int p, float PF,
+                                                          double* partial, unsigned int* arrived,
+                                                          int accumulate, double* out) {
   const uint32_t lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   double acc = 0.0;
-  for (int64_t i = blockIdx.x; i < nunits; i += gridDim.x) {
-    const Chunk ch = ld_chunk(chunks + (i >> units));
-    const int b = (static_cast<int>(i & ((1 << units) - 1)) * kWaves + wave) * U;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * W + wave; i < nunits;
+       i += static_cast<int64_t>(gridDim.x) * W) {
+    const Chunk ch = ld_chunk(chunks + (i >> shift));
+    const int b = static_cast<int>(i & ((1 << shift) - 1)) * U;
     const int left = ch.len - b * kStateBlock;
     if (left >= U * kStateBlock) {
       sumsq_blocks<U, GDT, STORE, ONE>(ch, gptrs, p, PF, b, lane, -1, acc);
@@ -100,7 +102,7 @@ __global__ __launch_bounds__(kBlock) void sumsq_kernel(const AwChunk* chunks,
       sumsq_blocks<1, GDT, STORE, ONE>(ch, gptrs, p, PF, b + k, lane, n, acc);
     }
   }
-  const double s = block_sum<kWaves>(acc);
+  const double s = block_sum<W>(acc);
   if constexpr (!JOIN) {
     if (threadIdx.x == 0) partial[blockIdx.x] = s;
   } else {
@@ -115,7 +117,7 @@ __global__ __launch_bounds__(kBlock) void sumsq_kernel(const AwChunk* chunks,
     acc = 0.0;
     if (threadIdx.x < gridDim.x)
       acc = __hip_atomic_load(partial + threadIdx.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const double total = block_sum<kWaves>(acc);
+    const double total = block_sum<W>(acc);
     if (threadIdx.x == 0) {
       *out = accumulate ? *out + total : total;
       __hip_atomic_store(arrived, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -254,41 +256,41 @@ void with_convert(int64_t n, int kind, F&& f) {
 }  // namespace
 
 hipError_t launch_sumsq(const SumsqLaunch& L) {
-  // entries of a small table are single units, which feed one block per wave
-  const bool four = L.p == 1 && L.units >= kLogOne;
-  const int units = four ? L.units - kLogOne : L.units;
-  const int64_t nunits = L.nchunks << units;
-  int64_t grid = static_cast<int64_t>(cu_count()) * (L.p == 1 ? kGroupsOne : kGroupsRanks);
-  if (nunits * L.p <= kJoinUnits) grid = kJoinMost;
+  const bool one = L.p == 1;
+  const int shift = one ? L.log_blocks - kLogOne : L.log_blocks;
+  const int64_t nunits = L.nchunks << shift;
+  const bool join = nunits <= kJoinMost * (one ? kJoinWaves * kJoinTurns : kWaves);
+  const int waves = one && join ? kJoinWaves : kWaves;
+  const int64_t most = join ? kJoinMost
+                            : static_cast<int64_t>(cu_count()) * (one ? kGroupsOne : kGroupsRanks);
+  int64_t grid = (nunits + waves - 1) / waves;
+  if (grid > most) grid = most;
   if (grid > kSumsqBlocks) grid = kSumsqBlocks;
-  if (grid > nunits) grid = nunits;
   if (grid < 1) grid = 1;  // no tensors: the sum is still written
   const float PF = static_cast<float>(static_cast<double>(L.p));
   with_gdt(L.gdt, [&](auto G) {
     constexpr int GDT = decltype(G)::value;
-    const dim3 gd(static_cast<unsigned>(grid)), bd(kBlock);
-    const auto go = [&](auto u, auto store, auto one, auto join) {
-      sumsq_kernel<decltype(u)::value, GDT, decltype(store)::value != 0,
-                   decltype(one)::value != 0, decltype(join)::value != 0>
-          <<<gd, bd, 0, L.stream>>>(L.chunks, L.gptrs, nunits, units, L.p, PF, L.partial,
+    const dim3 gd(static_cast<unsigned>(grid)), bd(static_cast<unsigned>(waves * kWave));
+    const auto go = [&](auto w, auto u, auto store, auto join_) {
+      constexpr int U = decltype(u)::value;
+      sumsq_kernel<decltype(w)::value, U, GDT, decltype(store)::value != 0, U == kLoadsOne,
+                   decltype(join_)::value != 0>
+          <<<gd, bd, 0, L.stream>>>(L.chunks, L.gptrs, nunits, shift, L.p, PF, L.partial,
                                     L.arrived, L.accumulate ? 1 : 0, L.out);
     };
     const auto pick = [&](auto store) {
-      const bool join = grid <= kJoinMost;
-      if (four)
-        join ? go(IC<kLoadsOne>{}, store, IC<1>{}, IC<1>{})
-             : go(IC<kLoadsOne>{}, store, IC<1>{}, IC<0>{});
-      else if (L.p == 1)
-        join ? go(IC<1>{}, store, IC<1>{}, IC<1>{}) : go(IC<1>{}, store, IC<1>{}, IC<0>{});
+      if (one)
+        join ? go(IC<kJoinWaves>{}, IC<kLoadsOne>{}, store, IC<1>{})
+             : go(IC<kWaves>{}, IC<kLoadsOne>{}, store, IC<0>{});
       else
-        join ? go(IC<1>{}, store, IC<0>{}, IC<1>{}) : go(IC<1>{}, store, IC<0>{}, IC<0>{});
+        join ? go(IC<kWaves>{}, IC<1>{}, store, IC<1>{}) : go(IC<kWaves>{}, IC<1>{}, store, IC<0>{});
     };
     L.store ? pick(IC<1>{}) : pick(IC<0>{});
   });
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || grid <= kJoinMost) return e;
+  if (e != hipSuccess || join) return e;
   sumsq_join_kernel<<<dim3(1), dim3(kJoinLanes), 0, L.stream>>>(L.partial, static_cast<int>(grid),
-                                                            L.accumulate ? 1 : 0, L.out);
+                                                                L.accumulate ? 1 : 0, L.out);
   return hipGetLastError();
 }
 

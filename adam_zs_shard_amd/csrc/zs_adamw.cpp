@@ -6,7 +6,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstring>
 #include <vector>
 
 #include "zs_adamw.h"
@@ -346,7 +345,6 @@ zs_status adamw_step(const zs_adamw_table* t, const zs_adamw_steps* steps,
   L.nchunks = t->nchunks;
   L.gdt = t->grad_dtype;
   L.pdt = t->param_dtype ? t->param_dtype : ZS_BF16;
-  L.bits = t->state_bits;
   L.rounding = hp->rounding;
   L.on_lines = t->on_lines != 0;
   L.stream = static_cast<hipStream_t>(stream);

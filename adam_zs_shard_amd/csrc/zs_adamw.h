@@ -13,7 +13,7 @@ constexpr int kStateBlock = ZS_STATE8_BLOCK;  // one wave: 64 lanes x 4 elements
 
 // A run of at most chunk_elems elements of one tensor, with every address at
 // its first element, so that a wave knows all it needs after one scalar load.
-constexpr int kUnit = 4 * kStateBlock;  // one workgroup of four waves
+constexpr int kUnit = 4 * kStateBlock;  // the shortest chunk, but for a tensor's last
 struct AwChunk {
   uint64_t w, m, v;           // addresses as numbers, see ld_chunk
   uint64_t m_scale, v_scale;
@@ -72,7 +72,7 @@ struct AwLaunch {
   AwArgs a;
   int64_t nchunks;
   int log_blocks;  // blocks of 256 elements per chunk, a power of two's exponent
-  int gdt, pdt, bits, rounding;
+  int gdt, pdt, rounding;
   bool on_lines;  // every tensor's arrays begin on a 128-byte line
   hipStream_t stream;
 };

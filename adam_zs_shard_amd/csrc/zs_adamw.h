@@ -10,10 +10,10 @@ constexpr int kF32 = ZS_F32;
 // A launch counts its lanes in 32 bits: 2^24 workgroups of 256 at most.
 constexpr int64_t kMaxGroups = (int64_t{1} << 24) - 1;
 constexpr int kStateBlock = ZS_STATE8_BLOCK;  // one wave: 64 lanes x 4 elements
+constexpr int kUnit = 4 * kStateBlock;  // the shortest chunk, but for a tensor's last
 
 // A run of at most chunk_elems elements of one tensor, with every address at
 // its first element, so that a wave knows all it needs after one scalar load.
-constexpr int kUnit = 4 * kStateBlock;  // the shortest chunk, but for a tensor's last
 struct AwChunk {
   uint64_t w, m, v;           // addresses as numbers, see ld_chunk
   uint64_t m_scale, v_scale;

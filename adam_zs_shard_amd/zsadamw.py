@@ -95,8 +95,11 @@ def _named(x, names) -> int:
     return names[x] if x.__class__ is str else int(x or 0)
 
 
-def hparams(lr, beta1, beta2, eps, step, *, grad_scale=1.0, max_norm=0.0, rounding="nearest",
+def hparams(lr, beta1, beta2, eps, step, *, grad_scale=1.0, max_norm=0.0, rounding="stochastic",
             seed=0, skip_nonfinite=False) -> zs_adamw_hparams:
+    """rounding: of 8-bit moments, "stochastic" or "nearest"; over a run, v does not follow its
+    gradient if it is rounded to nearest.  seed: of the random bits; the step is mixed in, so one
+    seed does for a run."""
     return zs_adamw_hparams(float(lr), float(beta1), float(beta2), float(eps), int(step),
                             float(grad_scale), float(max_norm), int(seed) & (2**64 - 1),
                             _named(rounding, ROUNDINGS), int(skip_nonfinite))

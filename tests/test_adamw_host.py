@@ -301,3 +301,49 @@ def test_step_tables_refuse():
                                      check=False) == z.ZS_ERR_ARG
     assert a.zs_adamw_step_multi_dev(_table(), steps(), a.hparams(**HP, max_norm=1.0), stream=0,
                                      check=False) == z.ZS_ERR_NULL
+
+
+# ---- rounding over a run ----------------------------------------------------------
+def test_moments_round_at_random_unless_told():
+    assert a.hparams(**HP).rounding == a.ZS_ROUND_STOCHASTIC
+    assert a.hparams(**HP, rounding="nearest").rounding == a.ZS_ROUND_NEAREST
+
+
+@pytest.mark.parametrize("beta2", [0.95, 0.99, 0.999])
+def test_rounding_of_v_over_a_run(beta2):
+    """300 steps of v from 1e-6 in blocks whose scale another element holds: with
+    a constant gradient, and with none.  Rounded to nearest, v never comes near
+    the square that it averages, and never decays; at random it follows both in
+    the mean."""
+    n, steps, u = 2048, 300, ref.U
+    g = np.full(n, np.sqrt(2.5e-6), np.float32)
+    g[1::2] = 0.0
+    g[::256] = 0.1
+    start = np.full(n, 1e-6, np.float32)
+    start[::256] = 1e-2
+    seen, gone = np.arange(n) % 2 == 0, np.arange(n) % 2 == 1
+    seen[::256] = False
+    want = np.float64(beta2) ** steps * 1e-6 + (1 - np.float64(beta2) ** steps) * g.astype(np.float64) ** 2
+    got = {}
+    for rounding in a.ROUNDINGS:
+        codes, scales = ref.encode(start, "v")
+        first = ref.decode(codes, scales, "v")
+        if rounding == "stochastic":  # its start as it is: the mean of many roundings
+            codes, scales = ref.encode(start, "v", ref.halves_for(n, 0, 0, 5)[1])
+        for t in range(1, steps + 1):
+            v = np.float32(beta2) * ref.decode(codes, scales, "v") + np.float32(1 - beta2) * (g * g)
+            halves = ref.halves_for(n, 0, t, 5)[1] if rounding == "stochastic" else None
+            codes, scales = ref.encode(v, "v", halves)
+        got[rounding] = ref.decode(codes, scales, "v").astype(np.float64)
+    # the scale's roundings alone move a code that stays: four a step, of a half step each
+    near = got["nearest"]
+    assert np.all(np.abs(near[gone] - first[gone]) <= 4 * steps * u * first[gone])
+    assert np.all((1 - beta2) * (want[seen] - near[seen]) <= near[seen] / 8)
+    assert np.all(near[seen] < 0.6 * 2.5e-6)
+    for which in (seen, gone):
+        x, w = got["stochastic"][which], want[which][0]
+        # five deviations of the mean; 16 bits leave 2^-17 of a spacing, v / 4 at most, at each step; v itself
+        # is at least the smallest code
+        least = 1e-2 * 2.0 ** -16 / 57344
+        slack = 2.0 ** -19 * max(w, 1e-6) / (1 - beta2) + 4 * steps * u * max(w, 1e-6)
+        assert abs(x.mean() - w) <= 5 * x.std() / np.sqrt(x.size) + slack + (least if w < 64 * least else 0)

@@ -731,3 +731,21 @@ def test_moments_move_between_the_forms():
     A.step_and_check(8)
     for b in A.all() + B.all():
         b.check("buffer")
+
+
+def test_default_rounding_follows_a_run():
+    """200 steps of 8-bit moments with the binding's own choice of rounding: the
+    mean of v stays at the square that it averages."""
+    n, steps, beta2 = 8192, 200, 0.95
+    M = Model([n], 1, "f32", None, 8, seed=98, states=False)
+    g = M.g[0][0]
+    g.fill_(2.5e-6 ** 0.5)
+    g[::256] = 0.1  # holds each block's scale
+    seen = np.arange(n) % 256 != 0
+    want = float(g[1]) ** 2 * (1 - beta2 ** steps)
+    for t in range(1, steps + 1):
+        a.zs_adamw_step_multi(M.table, a.hparams(LR, B1, beta2, EPS, t, seed=6))
+    v = M.host(0)["v"][seen].astype(np.float64)
+    # five deviations of the mean, and 2^-17 of a spacing (v / 4 at most) at each step; rounded to nearest, all of
+    # them end on one code, 2.3% off, with no deviation
+    assert abs(v.mean() - want) <= 5 * v.std() / np.sqrt(v.size) + want * (2.0 ** -19 / (1 - beta2) + 1e-4)

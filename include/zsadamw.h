@@ -49,14 +49,20 @@
  *     It is for conversions and for comparing; training takes the other.
  *   ZS_ROUND_STOCHASTIC: up or down with the probability that the place
  *     between the two neighbours says, so that the mean of what is stored is
- *     the value itself, and small steps add up.  The random
- *     bits are a function of (seed, element index, step) alone:
+ *     the value itself, and small steps add up.  (Not of a positive v below
+ *     the smallest code, 2^-16 / 57344 of its block's largest: it is held as
+ *     that code, since code 0 is not for it.)  The random bits come from
  *     Philox4x32-7 (Salmon et al., "Parallel random numbers: as easy as 1, 2,
  *     3", SC'11) with key = seed and counter = (index of the first of four
- *     elements, step); word j goes to element j, its low 16 bits r to m, its
- *     high 16 to v.  |y| (moved up by 2^-6 for m, 2^-14 for v, where it lies
- *     below that: the even part of the grid) has r * 2^(d-16) + 2^(d-17)
- *     added to its fp32 bits and the low d bits cut, d = 20 for m, 21 for v.
+ *     elements, step), the fours counted from the piece's first element; word
+ *     j goes to element j of the four, its low 16 bits r to m, its high 16 to
+ *     v.  So pieces that are cut out of a tensor at multiples of 4, with
+ *     indexes to match, get the bits of the whole, and at multiples of
+ *     ZS_STATE8_BLOCK its blocks, codes and scales too; cut elsewhere, their
+ *     bits are others, as good.  |y| (moved up by 2^-6 for m, 2^-14 for v,
+ *     where it lies below that: the even part of the grid) has
+ *     r * 2^(d-16) + 2^(d-17) added to its fp32 bits and the low d bits cut,
+ *     d = 20 for m, 21 for v.
  */
 #ifndef ZSADAMW_H
 #define ZSADAMW_H
@@ -88,7 +94,7 @@ typedef struct {
   double weight_decay;      /* finite, >= 0 */
   double lr_scale;          /* finite */
   int64_t index;            /* >= 0: index of element 0 for ZS_ROUND_STOCHASTIC, e.g. in the whole model
-                             * (elements of equal index share their random bits) */
+                             * (pieces of equal index share their random bits) */
 } zs_adamw_piece;
 
 /* Host-side handle of an uploaded table. */

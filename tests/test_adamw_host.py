@@ -347,3 +347,32 @@ def test_rounding_of_v_over_a_run(beta2):
         least = 1e-2 * 2.0 ** -16 / 57344
         slack = 2.0 ** -19 * max(w, 1e-6) / (1 - beta2) + 4 * steps * u * max(w, 1e-6)
         assert abs(x.mean() - w) <= 5 * x.std() / np.sqrt(x.size) + slack + (least if w < 64 * least else 0)
+
+
+def test_random_bits_of_cut_tensors():
+    """Fours of elements share a counter and are counted from the piece's first
+    one: a cut at a multiple of 4 leaves every element its bits."""
+    n, index, step, seed = 64, (1 << 33) + 6, 3, 11
+    whole = np.stack(ref.halves_for(n, index, step, seed))
+    for cut in (4, 8, 60):
+        first, rest = ref.halves_for(cut, index, step, seed), ref.halves_for(n - cut, index + cut, step, seed)
+        assert np.array_equal(np.concatenate([first, rest], 1), whole)
+    for cut in (1, 6, 63):
+        rest = np.stack(ref.halves_for(n - cut, index + cut, step, seed))
+        assert not np.any(np.all(rest == whole[:, cut:], 0))
+
+
+def test_random_rounding_of_v_below_the_smallest_code():
+    """A positive v below the smallest code always gets it; from there on, and
+    for m everywhere, the mean is kept."""
+    halves = np.arange(255, dtype=np.uint32) * 257
+    least = 2.0 ** -16 / 57344
+    for x, kept in ((1e-12, False), (0.9 * least, False), (1.5 * least, True)):
+        row = np.full(256, x, np.float32)
+        row[0] = 1.0
+        c, s = ref.encode(row, "v", np.concatenate([np.zeros(1, np.uint32), halves]))
+        back = ref.decode(c, s, "v")[1:].astype(np.float64)
+        assert np.all(c[1:] >= 1)
+        # 255 evenly spread halves: the share that rounds up is off by one of them at most
+        assert (abs(back.mean() - x) <= least / 254) == kept
+        assert kept or np.all(c[1:] == 1)

@@ -749,3 +749,30 @@ def test_default_rounding_follows_a_run():
     # five deviations of the mean, and 2^-17 of a spacing (v / 4 at most) at each step; rounded to nearest, all of
     # them end on one code, 2.3% off, with no deviation
     assert abs(v.mean() - want) <= 5 * v.std() / np.sqrt(v.size) + want * (2.0 ** -19 / (1 - beta2) + 1e-4)
+
+
+@pytest.mark.parametrize("p", [1, 3])
+def test_pieces_of_a_tensor_get_the_whole_ones_bits(p):
+    """A tensor stepped whole, and cut at multiples of 256 into pieces whose
+    indexes match: the same weights, codes and scales.  Cut elsewhere, a piece's
+    random bits are those of its own fours."""
+    n, cuts = 9000, [0, 256, 1280, 8192, 9000]
+    M, E = (Model([n], p, "bf16", "bf16", 8, seed=99) for _ in range(2))
+    q = E.pieces()[0]
+    parts = []
+    for lo, hi in zip(cuts, cuts[1:]):
+        b = slice(lo // 256, -(-hi // 256))
+        parts.append(dict(q, len=hi - lo, grads=[x[lo:hi] for x in q["grads"]], index=q["index"] + lo,
+                          **{k: q[k][lo:hi] for k in ("w", "m", "v", "param")},
+                          **{k: q[k][b] for k in ("m_scale", "v_scale")}))
+    ws = torch.empty(a.zs_adamw_workspace_bytes([x["len"] for x in parts], p), dtype=torch.uint8, device=DEV)
+    table = a.zs_adamw_upload(parts, p, "bf16", "bf16", 8, ws, ws.numel())
+    hp = a.hparams(LR, B1, B2, EPS, 12, rounding="stochastic", seed=21)
+    a.zs_adamw_step_multi(M.table, hp)
+    a.zs_adamw_step_multi(table, hp)
+    for x, y in zip(M.all(), E.all()):
+        assert np.array_equal(bits_of(x.flat), bits_of(y.flat))
+    N = Model([6, n - 6], p, "bf16", "bf16", 8, seed=99)
+    N.index = [M.index[0], M.index[0] + 6]
+    N.table = N.upload()
+    N.step_and_check(12, rounding="stochastic", seed=21)

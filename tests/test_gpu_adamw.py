@@ -2,6 +2,8 @@
 for bit with the stated fp32 sequence, and within the bounds that adamw_ref
 derives of the definition in 64 bits."""
 
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -776,3 +778,57 @@ def test_pieces_of_a_tensor_get_the_whole_ones_bits(p):
     N.index = [M.index[0], M.index[0] + 6]
     N.table = N.upload()
     N.step_and_check(12, rounding="stochastic", seed=21)
+
+
+def norm_and_means(M, launches):
+    """`launches` sums of squares in a row (the mean kept if M has it) against the
+    exact sum of the fp32 means' squares, which are exact in double.  The sizes
+    here put fewer than 64 roundings between an element and the sum: 32 on its
+    lane, 6 + 8 in its workgroup, as many in the join, one for what is there."""
+    means = [ref.mean32([b[i].float().cpu().numpy() for b in M.g]) for i in range(len(M.lens))]
+    want = math.fsum(float(s) for x in means for s in x.astype(np.float64) ** 2)
+    out = torch.full((launches + 2,), 7.0, dtype=torch.float64, device=DEV)
+    for k in range(launches):
+        if M.mean:
+            M.mean.fill([torch.full((n,), -1.0) for n in M.lens])
+        a.zs_grad_sumsq_multi(M.table, out[k + 1:], store_mean=bool(M.mean))
+        if M.mean:
+            for i, x in enumerate(means):
+                same(M.mean[i], x, f"mean of tensor {i}")
+            M.mean.check("mean")
+    got = out.cpu().numpy()
+    assert got[0] == 7.0 and got[-1] == 7.0
+    assert abs(got[1] - want) <= 64 * 2.0 ** -53 * want
+    assert np.all(got[1:-1] == got[1])
+    a.zs_grad_sumsq_multi(M.table, out, accumulate=True)
+    assert out[0].item() == 7.0 + got[1]
+    for b in M.g + M.all():
+        b.check("buffer")
+
+
+@pytest.mark.parametrize("grad,store,shift", [
+    ("bf16", False, 0), ("bf16", True, 3), ("f16", True, 0), ("f16", False, 1), ("f32", True, 1), ("f32", False, 0)])
+@pytest.mark.parametrize("lens", [[9 * 1024], [5, 1, 2050], [100_003, 5, 700, 257], [300_001, 300_002]])
+def test_sumsq_of_one_rank_in_one_launch(grad, store, shift, lens):
+    """2 to 64 workgroups that add their sums in the launch."""
+    norm_and_means(Model(lens, 1, grad, None, 32, shift, seed=100, mean=store, gscale=1e-2), 4)
+
+
+@pytest.mark.parametrize("grad,store", [("bf16", True), ("f32", False)])
+@pytest.mark.parametrize("entries", [1023, 1024, 1025])
+def test_sumsq_where_one_launch_becomes_two(grad, store, entries):
+    n = 1023 * 1024 + {1023: 0, 1024: 1, 1025: 1025}[entries]
+    M = Model([n], 1, grad, None, 32, None, seed=101, mean=store, gscale=1e-2)
+    assert M.table.nchunks == entries
+    norm_and_means(M, 2)
+
+
+@pytest.mark.parametrize("p,grad,store,shift,lens", [
+    (2, "bf16", True, 1, [61 * 1024, 1000]), (9, "f16", False, 0, [61 * 1024, 1000]),  # one
+    (2, "bf16", False, 0, [66 * 1024]), (9, "f16", True, 3, [66 * 1024]),              # two
+    (17, "f16", True, 3, [300_001, 7]), (17, "f16", False, 0, [300_001, 7]),
+    (64, "bf16", True, 0, [200_000, 100_003]), (64, "bf16", False, 5, [200_000, 100_003])])
+def test_sumsq_of_ranks_in_one_launch_and_two(p, grad, store, shift, lens):
+    M = Model(lens, p, grad, None, 32, shift, seed=102, mean=store, gscale=1e-2)
+    assert (M.table.nchunks <= 64) == (sum(lens) < 64 * 1024)
+    norm_and_means(M, 2)

@@ -376,3 +376,53 @@ def test_random_rounding_of_v_below_the_smallest_code():
         # 255 evenly spread halves: the share that rounds up is off by one of them at most
         assert (abs(back.mean() - x) <= least / 254) == kept
         assert kept or np.all(c[1:] == 1)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("decay,lr_scale", [(0.1, 1.0), (0.01, 1.0), (0.5, 0.5), (0.0, 2.0)])
+def test_reference_definition_is_torch_adamw(bits, decay, lr_scale):
+    """step64 against torch's AdamW in 64 bits, on weights up to some tens: both
+    are w - lr*u - lr*decay*w, so only 64-bit roundings lie between them."""
+    rng = np.random.default_rng(4)
+    n, lr, b1, b2, u64 = 3000, 1e-3, 0.9, 0.95, 2.0 ** -53
+    w = rng.standard_normal(n) * 10.0 ** rng.uniform(-2, 1.5, n)
+    p = torch.nn.Parameter(torch.from_numpy(w.copy()))
+    opt = torch.optim.AdamW([p], lr=lr * lr_scale, betas=(b1, b2), eps=1e-8, weight_decay=decay)
+    m, v, size, bound = np.zeros(n), np.zeros(n), np.zeros(n), np.zeros(n)
+    for t in range(1, 9):
+        g = rng.standard_normal(n) * 1e-2
+        p.grad = torch.from_numpy(g.copy())
+        opt.step()
+        h = dict(lr=lr * lr_scale, decay=decay, beta1=b1, beta2=b2, eps=1e-8, step=t, gs=1.0)
+        w, m, v, *_ = ref.step64([g], w, m, v, h, bits)
+        # on each side m is off by 4 roundings of its terms' sizes at each step (5 t in all), v by as many of itself;
+        # the quotient has the corrections, a root, a sum and a division besides, the weight two products and two
+        # sums: 40 (t + 1) and 8 cover both sides
+        size = b1 * size + (1 - b1) * np.abs(g)
+        most = size / (1 - b1 ** t) / (np.sqrt(v / (1 - b2 ** t)) + 1e-8)
+        bound += u64 * (40 * (t + 1) * lr * lr_scale * most + 8 * np.abs(w))
+        assert np.all(np.abs(p.detach().numpy() - w) <= bound)
+    # what a decay or a learning rate that is a tenth off would move is far above
+    assert np.all(bound < 1e-9 * (lr * lr_scale * most + np.abs(w)))
+    state = opt.state[p]
+    assert np.all(np.abs(state["exp_avg"].numpy() - m) <= 100 * u64 * size)
+    assert np.all(np.abs(state["exp_avg_sq"].numpy() - v) <= 100 * u64 * v)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_reference_sequence_stays_within_the_definition(bits):
+    """step32 and its bounds against step64, several ranks, clipped and scaled."""
+    rng = np.random.default_rng(5)
+    n = 3000
+    w = (rng.standard_normal(n) * 10.0 ** rng.uniform(-3, 1.5, n)).astype(np.float32)
+    m = (rng.standard_normal(n) * 1e-3).astype(np.float32)
+    v = (rng.standard_normal(n) ** 2 * 1e-5 + 1e-7).astype(np.float32)
+    grads = [(rng.standard_normal(n) * 1e-2).astype(np.float32) for _ in range(3)]
+    for decay, gs, t in ((0.1, 1.0, 1), (0.01, 0.3, 7), (0.5, -0.125, 1000)):
+        h = dict(lr=1e-3, decay=decay, beta1=0.9, beta2=0.95, eps=1e-8, step=t, gs=gs)
+        w32, m32, v32, *off = ref.step32(ref.mean32(grads), w, m, v, h, bits)
+        w64, m64, v64, bw, bm, bv = ref.step64(grads, w, m, v, h, bits)
+        for got, want, b in ((w32, w64, bw), (m32, m64, bm), (v32, v64, bv)):
+            assert np.all(np.abs(got - want) <= b)
+        # and the bound is below a thousandth of the move and a millionth of the weight
+        assert np.all(bw <= 1e-3 * np.abs(w64 - w) + 1e-6 * np.abs(w))

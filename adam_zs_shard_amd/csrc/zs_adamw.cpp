@@ -477,6 +477,8 @@ zs_status zs_grad_sumsq_multi(const zs_adamw_table* t, int32_t store_mean, int32
     if (store_mean && t->npieces > 0 && !t->has_mean) return ZS_ERR_NULL;
     const Layout lay = layout(t->nchunks, t->npieces, t->p);
     auto* base = static_cast<unsigned char*>(t->workspace);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(sumsq), ws = reinterpret_cast<uintptr_t>(base);
+    if (at < ws + lay.total && ws < at + sizeof(double)) return ZS_ERR_ALIAS;
     zs::SumsqLaunch L;
     L.chunks = reinterpret_cast<const zs::AwChunk*>(base + lay.chunks);
     L.gptrs = reinterpret_cast<const uint64_t*>(base + lay.gptrs);

@@ -210,7 +210,8 @@ zs_status zs_adamw_steps_status(const zs_adamw_steps* steps, int64_t* cursor, in
  * accumulate continues a norm over several tables.
  * Bytes per element: p gradients, + 4 with store_mean.
  * Errors: ZS_ERR_NULL (also store_mean where a tensor has no g_mean),
- * ZS_ERR_ARG, ZS_ERR_DTYPE, ZS_ERR_HIP. */
+ * ZS_ERR_ARG, ZS_ERR_DTYPE, ZS_ERR_ALIAS (sumsq lies in the table's
+ * workspace), ZS_ERR_HIP. */
 zs_status zs_grad_sumsq_multi(const zs_adamw_table* table, int32_t store_mean, int32_t accumulate,
                               double* sumsq, void* stream);
 

@@ -426,3 +426,15 @@ def test_reference_sequence_stays_within_the_definition(bits):
             assert np.all(np.abs(got - want) <= b)
         # and the bound is below a thousandth of the move and a millionth of the weight
         assert np.all(bw <= 1e-3 * np.abs(w64 - w) + 1e-6 * np.abs(w))
+
+
+@no_device
+def test_sumsq_refuses_its_own_workspace():
+    """The sum is written: over an entry of the table it would leave addresses
+    that the next launch follows."""
+    t = _table()
+    total = 4 * 128 + 256 + 256 + 2048 * 8  # entries, rank pointers, count, partial sums
+    for at in (0, 64, total - 8):
+        assert a.zs_grad_sumsq_multi(t, WS + at, stream=0, check=False) == z.ZS_ERR_ALIAS, at
+    for at in (-8, total):
+        assert a.zs_grad_sumsq_multi(t, WS + at, stream=0, check=False) != z.ZS_ERR_ALIAS, at

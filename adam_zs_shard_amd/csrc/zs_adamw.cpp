@@ -17,10 +17,16 @@ using zs::kMaxGroups;
 
 // Elements per entry of the launch table: 8192, or 1024 in tables of fewer than
 // 512 such or of tensors that are shorter on average: short tensors then launch
-// no idle waves (200,000 elements in 300 tensors, 32-bit moments: 3.7 us on the
-// GPU, 7.8 with 8192), and the norm's workgroups find a unit each (200,000
-// elements 4.6 us, 5.4).  1.0e9 elements with entries of 2048 / 4096 / 8192 /
-// 32,768: 5.06 / 5.05 / 5.03 / 5.04 ms (four waves per workgroup).
+// no idle waves (200,000 elements in 300 tensors, 32-bit moments 4.5 us, 9.1
+// with 8192; their norm 4.9, 5.4).  Both sizes on both sides of the 512, which
+// is 4.2M elements, 35 tensors, us with 1024 / 8192:
+//   elements                     1.0e6        4.0e6        8.0e6      1.6e7
+//   32 bits, one gradient     7.1 /  8.0  20.8 / 20.9  37.5 / 38.0   70 /  72
+//   32 bits, 8 ranks         10.2 / 12.2  30.0 / 30.0  57.8 / 57.0  112 / 111
+//   8 bits, 8 ranks          11.0 / 11.8  24.0 / 23.8  43.6 / 40.9   76 /  75
+//   norm, one gradient        6.0 /  5.3   6.7 /  6.6   8.9 /  8.1   12 /  11
+// 1.0e9 elements, one gradient: 4.29 / 4.35 ms, in a table of eight times the
+// bytes.
 constexpr int kUnitsLarge = 3, kUnitsSmall = 0;
 constexpr int64_t kChunkLarge = int64_t{zs::kUnit} << kUnitsLarge;
 constexpr int64_t kChunkSmall = int64_t{zs::kUnit} << kUnitsSmall;
@@ -95,8 +101,9 @@ struct Stream {
 // The elements (0..63) before the first chunk boundary of a tensor, chosen so
 // that from there on its arrays' accesses start as near to whole 128-byte
 // lines as they can.  1.0e9 elements with 32-bit moments in buffers that begin
-// 12 bytes into a line: 5.47 ms with chunks from the first element on, 4.83
-// with this (4.79 where all begin on a line).
+// 12 bytes into a line: 6.09 ms with chunks from the first element on, 4.32
+// with this (4.34 where all begin on a line); 30M, 3 ranks, 52 bytes into one:
+// 173 us and 158.
 int head_of(const std::vector<Stream>& streams) {
   int best = 0, best_score = -1;
   for (int h = 0; h < kHeadMost; ++h) {

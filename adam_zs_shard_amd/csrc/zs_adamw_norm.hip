@@ -62,17 +62,20 @@ __device__ __forceinline__ void sumsq_blocks(const Chunk& ch, const uint64_t* gp
 // writes back and invalidates its L2: with 1024 workgroups it cost 40 us (15.6M
 // elements, 8 ranks: 62 -> 105 us).  So at most kJoinMost workgroups do it: of
 // kJoinWaves waves each for one rank's sums of up to kJoinTurns turns of theirs
-// (1.0e6 elements: 5.2 us on the GPU and 4.6 on the host, against 5.0 and 7.6
-// in two launches; two more turns 8.0 us on the GPU; 50,000 elements 4.3, with
-// sixteen waves 5.2), of four waves for several ranks' sums of one turn.
+// (us on the GPU and on the host, against two launches: 50,000 elements 4.3 and
+// 4.7, 5.0 and 7.8; 500,000 4.7 and 4.4, 5.0 and 7.0; 1.0e6 6.1 and 4.5, 5.3 and
+// 6.9; with two more turns 2.0e6 8.5 and 4.4, 5.6 and 7.1; sixteen waves, once
+// tried, took 0.9 more at 50,000), of four waves for several ranks' sums of one
+// turn.
 constexpr int kJoinMost = 64, kJoinWaves = 8, kJoinTurns = 2;
 
 // One rank: four blocks per wave and turn, so that as many bytes are in
-// flight, four workgroups per CU (1.0e9 bf16 elements 299 us, 6.7 TB/s; two,
-// three and five 300 / 333 / 298, eight blocks 325, two 365).  More ranks: one
-// block of each, three workgroups per CU, so that the window swept at a time
-// stays narrow (60M elements, 8 ranks, the mean kept: 198 us, 6.05 TB/s; two,
-// four, five and eight 229 / 208 / 225 / 222, four blocks 214).
+// flight, four workgroups per CU (1.0e9 bf16 elements in a graph's replays 299
+// us, 6.7 TB/s, called in a row 285; replays with two, three and five 468 / 332
+// / 297, eight blocks 332, two 467).  More ranks: one block of each, three
+// workgroups per CU, so that the window swept at a time stays narrow (60M
+// elements, 8 ranks, the mean kept: 198 us, 6.07 TB/s; two, four and five 230 /
+// 206 / 224, eight and four blocks, once tried, 222 and 214).
 constexpr int kLogOne = 2;
 constexpr int kLoadsOne = 1 << kLogOne;
 constexpr int kGroupsOne = 4, kGroupsRanks = 3;
@@ -126,8 +129,8 @@ __global__ __launch_bounds__(W * kWave) void sumsq_kernel(const AwChunk* chunks,
 }
 static_assert(kJoinMost <= kBlock, "one sum per thread in the join");
 
-// One lane per sum on a card of 256 CUs (15.6M elements, 8 ranks 57.1 us in
-// all; 58.2 with 256 lanes).
+// One lane per sum on a card of 256 CUs (15.6M elements, 8 ranks 56.8 us in
+// all; 57.0 with 256 lanes).
 constexpr int kJoinLanes = 1024;
 
 __global__ __launch_bounds__(kJoinLanes) void sumsq_join_kernel(const double* partial, int n,
@@ -144,8 +147,10 @@ __global__ void steps_advance_kernel(AwStepsDev* t, const double* sumsq) {
 
 // Conversions: a wave takes U blocks of 256 values, its loads first.  Two where
 // there are enough for all CUs' waves: 117M values to 8 bits 93 us, 6.3 TB/s
-// (one 102, four 92), 1.0e9 from 8 bits 800 us (919, 963); one below
-// kConvertFew values: 50,000 from 8 bits 2.2 us (two 3.0).
+// (one 102), from 8 bits 83 (81), 1.0e9 to 8 bits 789 us (841), from 8 bits 795
+// (898); one below kConvertFew values.  Around it, us to / from 8 bits, two
+// blocks 3.8 / 3.2 at 2.0e6, 5.4 / 4.5 at 4.0e6 and 9.2 / 7.1 at 8.0e6, one
+// 3.4 / 3.2, 5.5 / 4.4 and 9.7 / 7.2; 50,000 values 2.2 / 2.8 and 1.9 / 2.1.
 constexpr int kConvertWaves = 8;
 constexpr int64_t kConvertFew = int64_t{1} << 21;
 

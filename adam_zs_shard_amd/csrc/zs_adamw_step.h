@@ -23,9 +23,9 @@ __device__ __forceinline__ void step_block(const AwArgs& a, const AwConsts& c, c
   Raw4<GDT> gq;
   if constexpr (ONE) {
     // a single gradient goes through plain loads beside 32-bit moments (1.0e9
-    // elements 4.79 -> 4.63 ms), non-temporal ones beside 8-bit moments
-    // (equal) and from several ranks (15.6M elements, 8 ranks 107.5 us, 110.2
-    // with plain ones)
+    // elements 4.32 ms, 4.48 with non-temporal ones), non-temporal ones beside
+    // 8-bit moments (2.63, plain 2.65) and from several ranks (15.6M elements,
+    // 8 ranks 106 us, 111 with plain ones)
     const char* gb = ch.g + e * kSize<GDT>;
     gq = n < 0 ? ld_raw4<GDT, BITS == 8>(gb, lane) : ld_raw4<GDT>(gb, lane, n);
   }
@@ -115,10 +115,10 @@ __device__ __forceinline__ void step_block(const AwArgs& a, const AwConsts& c, c
 
 // One block per wave, W waves per workgroup.  The grid sweeps the tensors in
 // order, so what is in flight at any moment is a narrow window of each array;
-// launch_step says which W keeps it narrowest.  (1.0e9 elements with 32-bit
-// moments and four waves: 4.96 ms this way, 5.12 with two blocks per wave,
-// 5.35 with eight; 8-bit moments and two waves: 2.53, 2.91 with two, 2.98
-// with four.)
+// launch_step says which W keeps it narrowest.  (More blocks per wave were
+// timed before W was chosen and the LDS below held waves back, 1.0e9 elements
+// with 32-bit moments: 4.96 ms with one block, 5.12 with two, 5.35 with eight;
+// and with 8-bit moments as they are now: 2.53, 2.91 with two, 2.98 with four.)
 template <int W, int GDT, int PDT, int BITS, bool RANDOM, bool ONE>
 __global__ __launch_bounds__(W * kWave) void adamw_kernel(AwArgs a) {
   const Chunk ch = ld_chunk(a.chunks + (blockIdx.x >> a.shift));
@@ -153,17 +153,20 @@ __global__ __launch_bounds__(W * kWave) void adamw_kernel(AwArgs a) {
 // Waves per workgroup, and LDS that a 32-bit step asks for and leaves alone so
 // that 16 waves share a CU instead of 32.  All figures with input sets that
 // take turns, as a training step's do; 1.0e9 elements except where stated.
-// 32-bit moments, one gradient: single waves, 16 of them: 4.33-4.38 ms (6.4-6.5
+// 32-bit moments, one gradient: single waves, 16 of them: 4.27-4.38 ms (6.4-6.6
 // TB/s); 12 / 14 / 20 / 24 / 32 per CU 4.78 / 4.61 / 4.43 / 4.54 / 4.68, two
 // waves per workgroup 4.47-4.49, four 4.63, eight 4.77.
 // 32-bit moments, several gradients: eight waves, two such workgroups on a CU:
 // 15.6M elements and 8 ranks 105.6 us (four waves 107.6, sixteen 112); from
 // kManyRanks on four waves, two such: 30M elements and 16 ranks 273 us against
-// 292, 15M and 64 ranks 399 against 423.
+// 292, 15M and 64 ranks 399 against 423.  Around the switch, 15M elements, eight
+// / four waves: 8 ranks 103 / 111, 12 ranks 125 / 128, 14 ranks 137 / 149, 16
+// ranks 143 / 142, 20 ranks 167 / 169, 24 ranks 185 / 185, 32 ranks 236 / 233.
 // 8-bit moments, as many waves as fit (they compute more per byte): with one
 // gradient two waves where all arrays begin on a line, 2.53 ms (four 2.56,
 // eight 2.57-2.61), else eight, 2.80 (two 3.24, four 2.99); with several
-// eight, 15.6M elements and 8 ranks 85.0 us (four 88.3, two 92.2).
+// eight, 15.6M elements and 8 ranks in buffers that begin 3 elements into a line
+// 85.0 us (four 88.3, two 92.2; on lines 74).  Of 64 ranks: 15M elements 380 us.
 // A small table's chunks have four blocks, which is four waves at most.
 constexpr unsigned kReserveOne = 160 * 1024 / 16 - 64, kReserveRanks = 160 * 1024 / 2 - 64;
 constexpr int kManyRanks = 16;

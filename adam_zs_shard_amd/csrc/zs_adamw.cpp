@@ -25,8 +25,9 @@ using zs::kMaxGroups;
 //   32 bits, 8 ranks         10.2 / 12.2  30.0 / 30.0  57.8 / 57.0  112 / 111
 //   8 bits, 8 ranks          11.0 / 11.8  24.0 / 23.8  43.6 / 40.9   76 /  75
 //   norm, one gradient        6.0 /  5.3   6.7 /  6.6   8.9 /  8.1   12 /  11
-// 1.0e9 elements, one gradient: 4.29 / 4.35 ms, in a table of eight times the
-// bytes.
+// (the norm of 1.0e6 is one launch with 1024 and two with 8192, which cost the
+// host 2.4 us more).  1.0e9 elements, 32 bits, one gradient: 4.29 / 4.35 ms, in a
+// table of eight times the bytes.
 constexpr int kUnitsLarge = 3, kUnitsSmall = 0;
 constexpr int64_t kChunkLarge = int64_t{zs::kUnit} << kUnitsLarge;
 constexpr int64_t kChunkSmall = int64_t{zs::kUnit} << kUnitsSmall;

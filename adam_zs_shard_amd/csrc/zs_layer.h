@@ -1,0 +1,99 @@
+// zs_layer.h -- the layer operators' launch descriptions (host and device).
+#pragma once
+
+#include "../../include/zslayer.h"
+#include "zs_adamw.h"
+
+namespace zs {
+
+// Rows of activations: the first element's address and the bytes between rows.
+struct Rows {
+  uintptr_t at;
+  int64_t pitch;
+};
+
+struct NormLaunch {
+  int64_t rows;
+  int cols;
+  int dt, wdt;
+  bool layer;
+  float eps;
+  Rows x, residual, total, y;  // residual.at 0: none
+  const void* gamma;           // or null
+  const void* beta;            // or null
+  float* mean;                 // or null
+  float* rstd;                 // or null
+  hipStream_t stream;
+};
+hipError_t launch_norm(const NormLaunch& L);
+
+// Workgroups of the norm's backward pass at most, each with one row of partial
+// sums per gradient in the workspace.
+constexpr int kNormParts = 512;
+
+struct NormGradLaunch {
+  int64_t rows;
+  int cols;
+  int dt, wdt, gdt;
+  bool layer, accumulate;
+  Rows dy, x, dres, dx;  // dres.at 0: none
+  const void* gamma;     // or null
+  const float* mean;
+  const float* rstd;
+  void* dgamma;          // or null
+  void* dbeta;           // or null
+  float* partial;        // kNormParts rows of dgamma's sums, then of dbeta's
+  hipStream_t stream;
+};
+hipError_t launch_norm_grad(const NormGradLaunch& L);
+
+struct EmbedLaunch {
+  int64_t tokens, rows, first_row, pos_rows;
+  int cols;
+  int dt, tdt;
+  bool wide_ids;  // 64-bit
+  float scale;
+  const void* ids;
+  const void* table;
+  const void* pos_ids;
+  const void* pos_table;  // or null
+  Rows y;
+  hipStream_t stream;
+};
+hipError_t launch_embed(const EmbedLaunch& L);
+
+// A token and the row of the table that it names (the table's number of rows:
+// none).
+struct TokenRow {
+  uint32_t row, token;
+};
+
+// Where the parts of an embedding gradient's workspace lie.
+struct EmbedLayout {
+  size_t a, b;     // the tokens, before and after a pass of the sort
+  size_t counts;   // of a pass's digits, per tile of the tokens
+  size_t partial;  // sums of rows whose tokens lie in several chunks
+  size_t total;
+};
+constexpr int kSortBits = 10;              // of a digit at most
+constexpr int kSortTile = 4096;            // tokens of a workgroup
+constexpr int64_t kSortAlone = 32768;      // tokens that one workgroup sorts at most
+// Chunks of the sorted tokens, each summed at a time.
+int embed_chunk(int64_t tokens, int64_t cols);
+EmbedLayout embed_layout(int64_t tokens, int64_t rows, int64_t cols);
+
+struct EmbedGradLaunch {
+  int64_t tokens, rows, first_row;
+  int cols;
+  int dt, gdt;
+  bool wide_ids, accumulate;
+  float scale;
+  const void* ids;
+  Rows dy;
+  void* grad;
+  unsigned char* workspace;
+  hipStream_t stream;
+};
+hipError_t launch_embed_grad(const EmbedGradLaunch& L);
+
+}  // namespace zs

@@ -103,7 +103,7 @@ zs_status norm_sizes(int64_t rows, int64_t cols, int32_t kind) {
 }
 
 size_t norm_workspace(int64_t cols) {
-  return sizeof(float) * 2 * static_cast<size_t>(kNormParts) * static_cast<size_t>(cols);
+  return sizeof(float) * 2 * kNormParts * static_cast<size_t>(zs::norm_width(static_cast<int>(cols)));
 }
 
 zs_status workspace_ok(const void* at, size_t bytes, size_t need) {
@@ -250,7 +250,7 @@ zs_status embed_backward(const zs_embed_grad_args* q) {
   if (q->tokens > 0) o.vector(q->ids, q->tokens, q->id_dtype == ZS_I64 ? 8 : 4, false);
   o.vector(q->grad, q->rows * q->cols, size_of(q->grad_dtype), true);
   if (q->tokens > 0) {
-    const size_t need = zs::embed_layout(q->tokens, q->rows, q->cols).total;
+    const size_t need = zs::embed_layout(q->tokens, q->cols).total;
     if (o.status() == ZS_OK)
       if (const zs_status st = workspace_ok(q->workspace, q->workspace_bytes, need)) return st;
     o.vector(q->workspace, static_cast<int64_t>(need), 1, true);
@@ -293,7 +293,8 @@ zs_status zs_embed_forward(const zs_embed_args* args) {
 }
 
 size_t zs_embed_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols) {
-  return embed_sizes(tokens, rows, cols) == ZS_OK ? zs::embed_layout(tokens, rows, cols).total : 0;
+  if (embed_sizes(tokens, rows, cols) != ZS_OK) return 0;
+  return zs::embed_layout(tokens > 0 ? tokens : 1, cols).total;
 }
 
 zs_status zs_embed_backward(const zs_embed_grad_args* args) {

@@ -30,6 +30,12 @@ hipError_t launch_norm(const NormLaunch& L);
 // Workgroups of the norm's backward pass at most, each with one row of partial
 // sums per gradient in the workspace.
 constexpr int kNormParts = 512;
+// Columns of such a row: what the lanes of a team hold, 8 or 16 columns each.
+constexpr int norm_width(int cols) {
+  int width = 512;
+  while (width < cols) width *= 2;
+  return width;
+}
 
 struct NormGradLaunch {
   int64_t rows;
@@ -42,7 +48,7 @@ struct NormGradLaunch {
   const float* rstd;
   void* dgamma;          // or null
   void* dbeta;           // or null
-  float* partial;        // kNormParts rows of dgamma's sums, then of dbeta's
+  float* partial;        // kNormParts rows of norm_width of dgamma's sums, then of dbeta's
   hipStream_t stream;
 };
 hipError_t launch_norm_grad(const NormGradLaunch& L);
@@ -70,17 +76,16 @@ struct TokenRow {
 
 // Where the parts of an embedding gradient's workspace lie.
 struct EmbedLayout {
-  size_t a, b;     // the tokens, before and after a pass of the sort
-  size_t counts;   // of a pass's digits, per tile of the tokens
-  size_t partial;  // sums of rows whose tokens lie in several chunks
+  size_t list;       // the tokens in the order of their rows
+  size_t other;      // the same before or after a pass of the sort
+  size_t counts;     // of a pass's digits, per tile of the tokens
+  size_t long_rows;  // rows whose tokens are summed in parts
+  size_t partial;    // these parts
   size_t total;
 };
-constexpr int kSortBits = 10;              // of a digit at most
-constexpr int kSortTile = 4096;            // tokens of a workgroup
-constexpr int64_t kSortAlone = 32768;      // tokens that one workgroup sorts at most
-// Chunks of the sorted tokens, each summed at a time.
-int embed_chunk(int64_t tokens, int64_t cols);
-EmbedLayout embed_layout(int64_t tokens, int64_t rows, int64_t cols);
+constexpr int kSortBits = 10;          // of a digit at most
+constexpr int64_t kSortAlone = 16384;  // tokens that one workgroup sorts at most
+EmbedLayout embed_layout(int64_t tokens, int64_t cols);
 
 struct EmbedGradLaunch {
   int64_t tokens, rows, first_row;

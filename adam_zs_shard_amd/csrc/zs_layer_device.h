@@ -25,10 +25,10 @@ struct Vals {
 };
 
 // The pack at `at`, or its first n elements and zeros behind them.
-template <int DT, bool STREAM = false>
+// Non-temporal unless STREAM is false.
+template <int DT, bool STREAM = true>
 __device__ __forceinline__ Pack<DT> ld_pack(const char* at) {
-  using T = decltype(Pack<DT>::x);
-  const T* p = reinterpret_cast<const T*>(at);
+  const auto* p = reinterpret_cast<const decltype(Pack<DT>::x)*>(at);
   return Pack<DT>{STREAM ? __builtin_nontemporal_load(p) : *p};
 }
 template <int DT>
@@ -46,11 +46,11 @@ __device__ __forceinline__ Pack<DT> ld_part(const char* at, int n) {
   }
   return q;
 }
-// n >= kPack: the whole pack; n <= 0: zeros, nothing read.
-template <int DT, bool STREAM = false>
+// n >= kPack: the whole pack; n <= 0: zeros, nothing read.  WHOLE: one of the two.
+template <int DT, bool WHOLE = false, bool STREAM = true>
 __device__ __forceinline__ Pack<DT> ld_some(const char* at, int n) {
   if (n >= kPack<DT>) return ld_pack<DT, STREAM>(at);
-  return n > 0 ? ld_part<DT>(at, n) : Pack<DT>{};
+  return !WHOLE && n > 0 ? ld_part<DT>(at, n) : Pack<DT>{};
 }
 
 template <int DT>
@@ -87,15 +87,11 @@ __device__ __forceinline__ Pack<DT> narrow(const float (&f)[kPack<DT>]) {
   return q;
 }
 
-template <int DT, bool STREAM = false>
+template <int DT, bool WHOLE = false>
 __device__ __forceinline__ void st_some(char* at, int n, const Pack<DT>& q) {
-  using T = decltype(Pack<DT>::x);
   if (n >= kPack<DT>) {
-    if constexpr (STREAM)
-      __builtin_nontemporal_store(q.x, reinterpret_cast<T*>(at));
-    else
-      *reinterpret_cast<T*>(at) = q.x;
-  } else if (n > 0) {
+    __builtin_nontemporal_store(q.x, reinterpret_cast<decltype(Pack<DT>::x)*>(at));
+  } else if (!WHOLE && n > 0) {
 #pragma unroll
     for (int i = 0; i < kPack<DT>; ++i)
       if (i < n) {
@@ -115,7 +111,7 @@ __device__ __forceinline__ Vals<V> ld_vals(const char* at, int n, float none) {
     if constexpr (WDT == kF32) {
 #pragma unroll
       for (int k = 0; k < V / 4; ++k) {
-        const Pack<kF32> q = ld_pack<kF32>(at + 16 * k);
+        const Pack<kF32> q = ld_pack<kF32, false>(at + 16 * k);
 #pragma unroll
         for (int i = 0; i < 4; ++i) r.v[4 * k + i] = q.x[i];
       }
@@ -143,6 +139,28 @@ __device__ __forceinline__ Vals<V> ld_vals(const char* at, int n, float none) {
     }
   }
   return r;
+}
+// Rounds V values to `at`, n of them there.
+template <int V, int DT>
+__device__ __forceinline__ void st_vals(char* at, int n, const Vals<V>& x) {
+  if constexpr (DT == kF32) {
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) {
+      const float f[4] = {x.v[4 * k], x.v[4 * k + 1], x.v[4 * k + 2], x.v[4 * k + 3]};
+      st_some<kF32>(at + 16 * k, n - 4 * k, narrow<kF32>(f));
+    }
+  } else if constexpr (V == 8) {
+    st_some<DT>(at, n, narrow<DT>(x.v));
+  } else {
+    const u32x2 q{narrow_pair<DT>(x.v[0], x.v[1]), narrow_pair<DT>(x.v[2], x.v[3])};
+    if (n >= 4) {
+      __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(at));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) reinterpret_cast<uint16_t*>(at)[i] = static_cast<uint16_t>(q[i / 2] >> (16 * (i % 2)));
+    }
+  }
 }
 // Of a vector of weights, from element c on; no vector: `none`.
 template <int V>

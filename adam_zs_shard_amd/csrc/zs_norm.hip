@@ -32,6 +32,16 @@ struct NormArgs {
   float eps;
 };
 
+template <int DT, int TEAM, int J, bool WHOLE, bool STREAM>
+__device__ __forceinline__ void ld_row(const Rows& rows, int64_t r, int lane, int cols, Pack<DT> (&q)[J]) {
+  const char* at = reinterpret_cast<const char*>(rows.at + r * rows.pitch);
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int c = (lane + j * TEAM) * kPack<DT>;
+    q[j] = ld_some<DT, WHOLE, STREAM>(at + c * kSize<DT>, cols - c);
+  }
+}
+
 // The sum over a team's lanes, in every one of them.  Between waves it goes
 // through part, two of which take turns, so that one barrier per sum will do:
 // who writes part k again has passed the barrier of part k + 1, before which
@@ -59,7 +69,7 @@ __device__ __forceinline__ void team_sums(float (&x)[N], float (*part)[N][16], i
   }
 }
 
-template <int DT, int TEAM, int E, int WG, bool LAYER>
+template <int DT, int TEAM, int E, int WG, bool LAYER, bool WHOLE, bool STREAM>
 __global__ __launch_bounds__(WG) void norm_kernel(NormArgs a) {
   constexpr int V = kPack<DT>, J = E / V, TEAMS = WG / TEAM;
   __shared__ float part[2][1][16];
@@ -78,23 +88,13 @@ __global__ __launch_bounds__(WG) void norm_kernel(NormArgs a) {
        r0 += static_cast<int64_t>(gridDim.x) * TEAMS) {
     const int64_t r = r0 + team;
     if (TEAMS > 1 && r >= a.rows) return;  // a team of one wave waits for nobody
-    const char* x = reinterpret_cast<const char*>(a.x.at + r * a.x.pitch);
     float t[J][V];
     Pack<DT> q[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const int c = (lane + j * TEAM) * V;
-      q[j] = ld_some<DT>(x + c * kSize<DT>, a.cols - c);
-    }
+    ld_row<DT, TEAM, J, WHOLE, STREAM>(a.x, r, lane, a.cols, q);
     if (a.residual.at) {
-      const char* res = reinterpret_cast<const char*>(a.residual.at + r * a.residual.pitch);
       char* total = reinterpret_cast<char*>(a.total.at + r * a.total.pitch);
       Pack<DT> p[J];
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int c = (lane + j * TEAM) * V;
-        p[j] = ld_some<DT>(res + c * kSize<DT>, a.cols - c);
-      }
+      ld_row<DT, TEAM, J, WHOLE, STREAM>(a.residual, r, lane, a.cols, p);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int c = (lane + j * TEAM) * V;
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(WG) void norm_kernel(NormArgs a) {
 #pragma unroll
         for (int i = 0; i < V; ++i) f[i] = t[j][i] + f[i];
         q[j] = narrow<DT>(f);
-        st_some<DT>(total + c * kSize<DT>, a.cols - c, q[j]);
+        st_some<DT, WHOLE>(total + c * kSize<DT>, a.cols - c, q[j]);
       }
     }
     float mean = 0.0f;
@@ -126,8 +126,8 @@ __global__ __launch_bounds__(WG) void norm_kernel(NormArgs a) {
       widen<DT>(q[j], t[j]);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if constexpr (LAYER) t[j][i] = i < left ? t[j][i] - mean : 0.0f;
-        s[0] += t[j][i] * t[j][i];
+        if constexpr (LAYER) t[j][i] = (WHOLE ? left > 0 : i < left) ? t[j][i] - mean : 0.0f;
+        s[0] = __builtin_fmaf(t[j][i], t[j][i], s[0]);
       }
     }
     team_sums<TEAM>(s, part, turn);
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(WG) void norm_kernel(NormArgs a) {
       float f[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = (t[j][i] * rstd) * gamma[j].v[i] + beta[j].v[i];
-      st_some<DT>(y + c * kSize<DT>, a.cols - c, narrow<DT>(f));
+      st_some<DT, WHOLE>(y + c * kSize<DT>, a.cols - c, narrow<DT>(f));
     }
     if (lane == 0) {
       if (LAYER && a.mean) a.mean[r] = mean;
@@ -164,7 +164,7 @@ struct GradRow {
   float mean, rstd;
 };
 
-template <int DT, int TEAM, int J, bool LAYER>
+template <int DT, int TEAM, int J, bool LAYER, bool WHOLE>
 __device__ __forceinline__ GradRow<DT, J> ld_grad_row(const NormGradArgs& a, int64_t r, int lane) {
   GradRow<DT, J> g{};
   if (r >= a.rows) return g;
@@ -173,19 +173,46 @@ __device__ __forceinline__ GradRow<DT, J> ld_grad_row(const NormGradArgs& a, int
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c = (lane + j * TEAM) * kPack<DT>;
-    g.dy[j] = ld_some<DT>(dy + c * kSize<DT>, a.cols - c);
-    g.x[j] = ld_some<DT>(x + c * kSize<DT>, a.cols - c);
+    g.dy[j] = ld_some<DT, WHOLE>(dy + c * kSize<DT>, a.cols - c);
+    g.x[j] = ld_some<DT, WHOLE>(x + c * kSize<DT>, a.cols - c);
   }
   if constexpr (LAYER) g.mean = a.mean[r];
   g.rstd = a.rstd[r];
   return g;
 }
 
-template <int DT, int TEAM, int E, int WG, bool LAYER, bool BETA>
+// Makes the compiler forget what it computed of a pack.
+template <int DT>
+__device__ __forceinline__ void forget(Pack<DT>& q) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    auto x = q.x[i];
+    asm volatile("" : "+v"(x));
+    q.x[i] = x;
+  }
+}
+
+// h = (x - mean) * rstd of a pack, zeros where the row has ended: 0 * rstd would
+// be NaN there if rstd is not finite.
+template <int DT, bool LAYER, bool WHOLE>
+__device__ __forceinline__ void normed(const Pack<DT>& x, float mean, float rstd, int left,
+                                       float (&h)[kPack<DT>]) {
+  widen<DT>(x, h);
+#pragma unroll
+  for (int i = 0; i < kPack<DT>; ++i) {
+    if constexpr (LAYER) h[i] = h[i] - mean;
+    h[i] = (WHOLE ? left > 0 : i < left) ? h[i] * rstd : 0.0f;
+  }
+}
+
+// A lane's sums go to place (j * V + i) * TEAM + lane of a row of sums, so that
+// all accesses of LDS and of the workspace are of neighbouring lanes; the join
+// puts them in the order of the columns.
+template <int DT, int TEAM, int E, int WG, bool LAYER, bool BETA, bool WHOLE>
 __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
   constexpr int V = kPack<DT>, J = E / V, TEAMS = WG / TEAM;
   __shared__ float part[2][LAYER ? 2 : 1][16];
-  extern __shared__ float sums[];  // cols, where there are several teams
+  extern __shared__ float sums[];  // WG * E, where there are several teams
   int turn = 0;
   const int lane = threadIdx.x % TEAM;
   const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM);
@@ -201,27 +228,31 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
   const float n = static_cast<float>(a.cols);
   const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
   int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
-  GradRow<DT, J> next = ld_grad_row<DT, TEAM, J, LAYER>(a, r, lane);
   // every team of the workgroup makes as many turns as its first
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * TEAMS; r0 < a.rows; r0 += step, r += step) {
-    const GradRow<DT, J> g = next;
-    next = ld_grad_row<DT, TEAM, J, LAYER>(a, r + step, lane);
-    float h[J][V], t[J][V];
+    GradRow<DT, J> g = ld_grad_row<DT, TEAM, J, LAYER, WHOLE>(a, r, lane);
+    Pack<DT> dres[J];
+    if (a.dres.at && r < a.rows) {
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int c = (lane + j * TEAM) * V;
+        dres[j] = ld_some<DT, WHOLE>(reinterpret_cast<const char*>(a.dres.at + r * a.dres.pitch) + c * kSize<DT>,
+                              a.cols - c);
+      }
+    }
     float s[LAYER ? 2 : 1] = {};
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      const int left = a.cols - (lane + j * TEAM) * V;
-      widen<DT>(g.x[j], h[j]);
-      widen<DT>(g.dy[j], t[j]);
+      float h[V], t[V];
+      normed<DT, LAYER, WHOLE>(g.x[j], g.mean, g.rstd, a.cols - (lane + j * TEAM) * V, h);
+      widen<DT>(g.dy[j], t);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        if constexpr (LAYER) h[j][i] = h[j][i] - g.mean;
-        h[j][i] = i < left ? h[j][i] * g.rstd : 0.0f;
-        acc_g[j][i] += t[j][i] * h[j][i];
-        if constexpr (BETA) acc_b[j][i] += t[j][i];
-        t[j][i] = t[j][i] * gamma[j].v[i];
-        s[0] += t[j][i] * h[j][i];
-        if constexpr (LAYER) s[1] += t[j][i];
+        acc_g[j][i] = __builtin_fmaf(t[i], h[i], acc_g[j][i]);
+        if constexpr (BETA) acc_b[j][i] += t[i];
+        t[i] = t[i] * gamma[j].v[i];
+        s[0] = __builtin_fmaf(t[i], h[i], s[0]);
+        if constexpr (LAYER) s[1] += t[i];
       }
     }
     team_sums<TEAM>(s, part, turn);
@@ -230,50 +261,45 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
     char* dx = reinterpret_cast<char*>(a.dx.at + r * a.dx.pitch);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
+      // h and dy * gamma once more: to keep them would take 2 E registers
       const int c = (lane + j * TEAM) * V;
-      float f[V];
+      float h[V], t[V];
+      forget(g.x[j]);
+      forget(g.dy[j]);
+      normed<DT, LAYER, WHOLE>(g.x[j], g.mean, g.rstd, a.cols - c, h);
+      widen<DT>(g.dy[j], t);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float u = LAYER ? t[j][i] - c1 : t[j][i];
-        f[i] = (u - h[j][i] * c2) * g.rstd;
+        t[i] = t[i] * gamma[j].v[i];
+        if constexpr (LAYER) t[i] = t[i] - c1;
+        t[i] = (t[i] - h[i] * c2) * g.rstd;
       }
       if (a.dres.at) {
-        const char* dres = reinterpret_cast<const char*>(a.dres.at + r * a.dres.pitch);
-        float d[V];
-        widen<DT>(ld_some<DT>(dres + c * kSize<DT>, a.cols - c), d);
+        widen<DT>(dres[j], h);
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = f[i] + d[i];
+        for (int i = 0; i < V; ++i) t[i] = t[i] + h[i];
       }
-      st_some<DT>(dx + c * kSize<DT>, a.cols - c, narrow<DT>(f));
+      st_some<DT, WHOLE>(dx + c * kSize<DT>, a.cols - c, narrow<DT>(t));
     }
   }
   if (!a.partial) return;
   const auto out = [&](float(&acc)[J][V], float* to) {
     if constexpr (TEAMS == 1) {
 #pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int c = (lane + j * TEAM) * V + i;
-          if (c < a.cols) to[c] = acc[j][i];
-        }
+      for (int k = 0; k < E; ++k) to[k * TEAM + lane] = acc[k / V][k % V];
     } else {
-      for (int k = 0; k < TEAMS; ++k) {
-        __syncthreads();
-        if (team != k) continue;
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const int c = (lane + j * TEAM) * V + i;
-            if (c < a.cols) sums[c] = k == 0 ? acc[j][i] : sums[c] + acc[j][i];
-          }
-      }
+      for (int k = 0; k < E; ++k) sums[(team * E + k) * TEAM + lane] = acc[k / V][k % V];
       __syncthreads();
-      for (int c = threadIdx.x; c < a.cols; c += WG) to[c] = sums[c];
+      for (int c = threadIdx.x; c < E * TEAM; c += WG) {
+        float s = sums[c];
+#pragma unroll
+        for (int k = 1; k < TEAMS; ++k) s += sums[k * E * TEAM + c];
+        to[c] = s;
+      }
     }
   };
-  float* to = a.partial + static_cast<int64_t>(blockIdx.x) * a.cols;
+  float* to = a.partial + static_cast<int64_t>(blockIdx.x) * (E * TEAM);
   out(acc_g, to);
   if constexpr (BETA) {
     if (TEAMS > 1) __syncthreads();
@@ -281,16 +307,16 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
   }
 }
 
-// The rows of sums, added in their order: 32 columns and 32 parts of the rows
-// per workgroup.
-constexpr int kJoinCols = 32, kJoinParts = 32;
+// The rows of sums, added in a fixed order: 16 places and 64 parts of the rows
+// per workgroup, eight loads of a lane in flight.
+constexpr int kJoinCols = 16, kJoinParts = 64, kJoinLoads = kNormParts / kJoinParts;
 
 struct NormJoinArgs {
   const float* partial;
   int64_t beta_at;
   void* dgamma;
   void* dbeta;
-  int parts, cols, dt, accumulate;
+  int parts, width, team, pack, cols, dt, accumulate;  // width: of a row of sums
 };
 
 __global__ __launch_bounds__(kJoinCols* kJoinParts) void norm_join_kernel(NormJoinArgs a) {
@@ -299,32 +325,57 @@ __global__ __launch_bounds__(kJoinCols* kJoinParts) void norm_join_kernel(NormJo
   void* to = beta ? a.dbeta : a.dgamma;
   if (!to) return;
   const int k = threadIdx.x % kJoinCols, p = threadIdx.x / kJoinCols;
-  const int c = blockIdx.x * kJoinCols + k;
-  const float* from = a.partial + (beta ? a.beta_at : 0);
-  float s = 0.0f;
-  if (c < a.cols)
-    for (int i = p; i < a.parts; i += kJoinParts) s += from[static_cast<int64_t>(i) * a.cols + c];
-  sums[p][k] = s;
-  __syncthreads();
-  if (p != 0 || c >= a.cols) return;
+  const int at = blockIdx.x * kJoinCols + k;  // width is a multiple of kJoinCols
+  const int own = at / a.team, c = (at % a.team + own / a.pack * a.team) * a.pack + own % a.pack;
+  const float* from = a.partial + (beta ? a.beta_at : 0) + at;
+  float x[kJoinLoads];
 #pragma unroll
-  for (int i = 1; i < kJoinParts; ++i) s += sums[i][k];
+  for (int i = 0; i < kJoinLoads; ++i) {
+    const int row = p + i * kJoinParts;
+    x[i] = row < a.parts && c < a.cols ? from[static_cast<int64_t>(row) * a.width] : 0.0f;
+  }
+  float s = x[0];
+#pragma unroll
+  for (int i = 1; i < kJoinLoads; ++i) s += x[i];
+  sums[p][k] = s;
+#pragma unroll
+  for (int d = kJoinParts / 2; d > 0; d /= 2) {
+    __syncthreads();
+    if (p < d) sums[p][k] = s = s + sums[p + d][k];
+  }
+  if (p != 0 || c >= a.cols) return;
   st_value(to, a.dt, c, a.accumulate ? ld_value(to, a.dt, c) + s : s);
 }
 
-// Calls f(dtype, team, elements per lane).
-template <class F>
+// Calls f(dtype, team, elements per lane) for the smallest team that holds a row.
+// A lane of the backward pass holds 8 elements (16 of the longest rows), so that
+// its sums leave registers for 16 waves per CU.  The forward pass takes 16, half
+// the waves per row (16384 x 4096 bf16, layer norm 47.8 us; 63.9 with 8).
+template <int E, class F>
 void with_shape(int dt, int cols, F&& f) {
   with_gdt(dt, [&](auto d) {
-    if (cols <= 512) f(d, IC<64>{}, IC<8>{});
-    else if (cols <= 1024) f(d, IC<64>{}, IC<16>{});
-    else if (cols <= 2048) f(d, IC<128>{}, IC<16>{});
-    else if (cols <= 4096) f(d, IC<256>{}, IC<16>{});
-    else if (cols <= 8192) f(d, IC<512>{}, IC<16>{});
+    if (cols <= 64 * 8) f(d, IC<64>{}, IC<8>{});
+    else if (cols <= 64 * E) f(d, IC<64>{}, IC<E>{});
+    else if (cols <= 128 * E) f(d, IC<128>{}, IC<E>{});
+    else if (cols <= 256 * E) f(d, IC<256>{}, IC<E>{});
+    else if (cols <= 512 * E) f(d, IC<512>{}, IC<E>{});
+    else if (cols <= 1024 * E) f(d, IC<1024>{}, IC<E>{});
     else f(d, IC<1024>{}, IC<16>{});
   });
 }
 static_assert(ZS_NORM_MAX_COLS == 1024 * 16, "the longest row is a team of 1024 lanes");
+
+// Workgroups of the forward pass: with a residual one row per team, which ends
+// (16384 x 4096 bf16 85.9 us, 6.2 TB/s; 92.9 with 1024 lanes per CU that go on to
+// further rows); without one, and for rows of 1024 lanes, as many elements per CU
+// at a time (16384 x 4096 bf16, layer norm 47.8 us, one row per team 52.0; 4096 x
+// 16384 56.9 and 70.9).
+constexpr int kNormHeld = 16384;
+// Where a call reads and writes more than this, its rows do not stay in the 256 MB
+// cache from one kernel of a model to the next, and it reads past that (16384 x 4096 with a
+// residual 85.9 us, 89.8 read through it); smaller ones may have been left there
+// by the kernel before (32768 x 1024 bf16 22.4 us, read past it 27.4).
+constexpr int64_t kNormCached = int64_t{192} << 20;
 
 constexpr int norm_group(int team) { return team == kWave ? 4 * kWave : team; }
 constexpr int grad_group(int team) { return team > 512 ? team : 512; }
@@ -345,15 +396,23 @@ hipError_t launch_norm(const NormLaunch& L) {
   a.cols = L.cols;
   a.wdt = L.wdt;
   a.eps = L.eps;
-  with_shape(L.dt, L.cols, [&](auto d, auto team, auto e) {
+  const bool stream = L.rows * L.cols * (L.dt == kF32 ? 4 : 2) * (L.residual.at ? 4 : 2) > kNormCached;
+  with_shape<16>(L.dt, L.cols, [&](auto d, auto team, auto e) {
     constexpr int TEAM = decltype(team)::value, WG = norm_group(TEAM), TEAMS = WG / TEAM;
     const int64_t groups = (L.rows + TEAMS - 1) / TEAMS;
-    const int64_t most = static_cast<int64_t>(cu_count()) * (2048 / WG);
+    const int64_t most = L.residual.at && TEAM < 1024 ? kMaxGroups
+                                                     : int64_t{cu_count()} * (kNormHeld / decltype(e)::value / WG);
     const dim3 grid(static_cast<unsigned>(groups < most ? groups : most));
-    if (L.layer)
-      norm_kernel<decltype(d)::value, TEAM, decltype(e)::value, WG, true><<<grid, WG, 0, L.stream>>>(a);
-    else
-      norm_kernel<decltype(d)::value, TEAM, decltype(e)::value, WG, false><<<grid, WG, 0, L.stream>>>(a);
+    const auto go = [&](auto layer, auto whole, auto past) {
+      norm_kernel<decltype(d)::value, TEAM, decltype(e)::value, WG, decltype(layer)::value != 0,
+                  decltype(whole)::value != 0, decltype(past)::value != 0><<<grid, WG, 0, L.stream>>>(a);
+    };
+    const auto pick = [&](auto whole, auto past) {
+      L.layer ? go(IC<1>{}, whole, past) : go(IC<0>{}, whole, past);
+    };
+    if (L.cols % kPack<decltype(d)::value> != 0) pick(IC<0>{}, IC<0>{});
+    else if (stream) pick(IC<1>{}, IC<1>{});
+    else pick(IC<1>{}, IC<0>{});
   });
   return hipGetLastError();
 }
@@ -370,39 +429,44 @@ hipError_t launch_norm_grad(const NormGradLaunch& L) {
   a.rstd = L.rstd;
   a.partial = sums ? L.partial : nullptr;
   a.rows = L.rows;
-  a.beta_at = static_cast<int64_t>(kNormParts) * L.cols;
   a.cols = L.cols;
   a.wdt = L.wdt;
-  int parts = 0;
-  if (L.rows > 0) {
-    with_shape(L.dt, L.cols, [&](auto d, auto team, auto e) {
+  NormJoinArgs j;
+  j.parts = 0;
+  {
+    with_shape<8>(L.dt, L.cols, [&](auto d, auto team, auto e) {
       constexpr int TEAM = decltype(team)::value, WG = grad_group(TEAM), TEAMS = WG / TEAM;
       const int64_t groups = (L.rows + TEAMS - 1) / TEAMS;
       int64_t most = static_cast<int64_t>(cu_count()) * (1024 / WG);
       if (most > kNormParts) most = kNormParts;
-      parts = static_cast<int>(groups < most ? groups : most);
-      const size_t lds = TEAMS > 1 ? sizeof(float) * static_cast<size_t>(L.cols) : 0;
-      const auto go = [&](auto layer, auto beta) {
+      j.parts = static_cast<int>(groups < most ? groups : most);
+      j.team = TEAM;
+      j.pack = kPack<decltype(d)::value>;
+      j.width = decltype(e)::value * TEAM;
+      a.beta_at = j.beta_at = static_cast<int64_t>(kNormParts) * j.width;
+      if (j.parts == 0) return;
+      const size_t lds = TEAMS > 1 ? sizeof(float) * decltype(e)::value * WG : 0;
+      const auto go = [&](auto layer, auto beta, auto whole) {
         norm_grad_kernel<decltype(d)::value, TEAM, decltype(e)::value, WG, decltype(layer)::value != 0,
-                         decltype(beta)::value != 0>
-            <<<dim3(static_cast<unsigned>(parts)), WG, lds, L.stream>>>(a);
+                         decltype(beta)::value != 0, decltype(whole)::value != 0>
+            <<<dim3(static_cast<unsigned>(j.parts)), WG, lds, L.stream>>>(a);
       };
-      L.layer ? go(IC<1>{}, IC<1>{}) : L.dbeta ? go(IC<0>{}, IC<1>{}) : go(IC<0>{}, IC<0>{});
+      const auto pick = [&](auto whole) {
+        L.layer ? go(IC<1>{}, IC<1>{}, whole) : L.dbeta ? go(IC<0>{}, IC<1>{}, whole) : go(IC<0>{}, IC<0>{}, whole);
+      };
+      L.cols % kPack<decltype(d)::value> == 0 ? pick(IC<1>{}) : pick(IC<0>{});
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (!sums || (L.rows == 0 && L.accumulate)) return hipSuccess;
-  NormJoinArgs j;
   j.partial = L.partial;
-  j.beta_at = a.beta_at;
   j.dgamma = L.dgamma;
   j.dbeta = L.dbeta;
-  j.parts = parts;
   j.cols = L.cols;
   j.dt = L.gdt;
   j.accumulate = L.accumulate ? 1 : 0;
-  norm_join_kernel<<<dim3(static_cast<unsigned>((L.cols + kJoinCols - 1) / kJoinCols), L.dbeta ? 2 : 1),
+  norm_join_kernel<<<dim3(static_cast<unsigned>(j.width / kJoinCols), L.dbeta ? 2 : 1),
                      kJoinCols * kJoinParts, 0, L.stream>>>(j);
   return hipGetLastError();
 }

@@ -475,7 +475,7 @@ def test_embed_grad_of_whole_numbers(kind, accumulate):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("tokens", [16_384, 32_768, 32_769, 40_000, 65_536, 131_073])
+@pytest.mark.parametrize("tokens", [16_384, 16_385, 32_768, 32_769, 40_000, 65_536, 131_073])
 def test_embed_grad_of_long_batches(kind, tokens):
     run_embed_grad(tokens, 3001, 24, kind, whole_numbers=True, seed=tokens, accumulate=tokens % 2 == 0)
     run_embed_grad(tokens, 70_000, 5, kind, whole_numbers=True, seed=tokens, accumulate=tokens % 2 == 1)

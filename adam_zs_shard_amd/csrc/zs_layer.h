@@ -83,8 +83,10 @@ struct EmbedLayout {
   size_t partial;    // these parts
   size_t total;
 };
-constexpr int kSortBits = 10;          // of a digit at most
-constexpr int64_t kSortAlone = 16384;  // tokens that one workgroup sorts at most
+// Tokens that are sorted in one launch at most, and the bits of a digit at most,
+// in that launch and in several.
+constexpr int64_t kSortAlone = 16384;
+constexpr int kBucketBits = 8, kSortBits = 10;
 EmbedLayout embed_layout(int64_t tokens, int64_t cols);
 
 struct EmbedGradLaunch {

@@ -14,10 +14,11 @@
  *
  * Numerics.  Every element is widened to fp32 and each output rounded once, to
  * nearest even.  The fp32 operations are those written below, each rounded
- * (no FMA contraction, correctly rounded division and root); sums over a row
- * or over rows are fp32 sums in an order that is fixed by the call's sizes,
- * strides, alignment and the device: the same bits every time.  Infinities and
- * NaN propagate by IEEE rules, within their row and into the gradients' sums.
+ * once (correctly rounded division and root); only a product that goes straight
+ * into a sum over a row or over rows is not rounded before it is added.  Such
+ * sums are in an order that is fixed by the call's sizes and the device: the
+ * same bits every time.  Infinities and NaN propagate by IEEE rules, within
+ * their row and into the gradients' sums.
  *
  * Rows of activations are row-major with a stride in elements, at least cols;
  * what lies between two rows is neither read nor written.  Element types are

@@ -475,7 +475,7 @@ def test_embed_grad_of_whole_numbers(kind, accumulate):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("tokens", [16_384, 16_385, 32_768, 32_769, 40_000, 65_536, 131_073])
+@pytest.mark.parametrize("tokens", [16_384, 16_385, 32_768, 32_769, 40_000, 65_536, 131_072, 131_073, 600_000])
 def test_embed_grad_of_long_batches(kind, tokens):
     run_embed_grad(tokens, 3001, 24, kind, whole_numbers=True, seed=tokens, accumulate=tokens % 2 == 0)
     run_embed_grad(tokens, 70_000, 5, kind, whole_numbers=True, seed=tokens, accumulate=tokens % 2 == 1)
@@ -497,7 +497,7 @@ def test_embed_grad_of_many_rows():
     for rows in (1 << 10, (1 << 20) - 1, 1 << 20, (1 << 20) + 5, 5_000_000):
         ids = torch.tensor([rows - 1, 0, rows // 2, rows - 1, rows - 2, -1, rows, 0])
         dy = torch.randint(-4, 5, (8, 4), generator=gen(rows)).float()
-        for n in (8, 8 * 5000):        # one workgroup's sort, and many
+        for n in (8, 8 * 5000, 8 * 20_000):        # in one launch, and in several
             G = torch.full((rows, 4), 7.0, device=DEV)
             nb = a.zs_embed_workspace_bytes(n, rows, 4)
             a.zs_embed_backward(n, ids.repeat(n // 8).to(DEV), rows, 4, dy.repeat(n // 8, 1).to(DEV), G, garbage(nb), nb)

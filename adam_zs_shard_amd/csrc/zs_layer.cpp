@@ -152,6 +152,7 @@ zs_status norm_backward(const zs_norm_grad_args* q) {
   if (const zs_status st = norm_sizes(q->rows, q->cols, q->kind)) return st;
   if ((q->accumulate != 0 && q->accumulate != 1) || q->reserved != 0) return ZS_ERR_ARG;
   if (!dtype_ok(q->dtype) || !dtype_ok(q->w_dtype) || !dtype_ok(q->grad_dtype)) return ZS_ERR_DTYPE;
+  if (q->rows == 0 && (q->accumulate || (!q->dgamma && !q->dbeta))) return ZS_OK;
   const int64_t size = size_of(q->dtype), gsize = size_of(q->grad_dtype);
   const bool layer = q->kind == ZS_NORM_LAYER;
   zs::NormGradLaunch L{};

@@ -459,7 +459,7 @@ hipError_t launch_norm_grad(const NormGradLaunch& L) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (!sums || (L.rows == 0 && L.accumulate)) return hipSuccess;
+  if (!sums) return hipSuccess;
   j.partial = L.partial;
   j.dgamma = L.dgamma;
   j.dbeta = L.dbeta;

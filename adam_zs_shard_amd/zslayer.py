@@ -10,6 +10,7 @@ fallback.
 from __future__ import annotations
 
 import ctypes as C
+import struct
 
 from . import zshard as z
 from .zsadamw import DTYPE_NAMES, ZS_F32, _named
@@ -86,51 +87,60 @@ def lib():
 
 
 # ----------------------------------------------------------------- marshalling
+# The argument structs are packed as bytes, which takes 1 us; 3 us as instances of
+# the classes above (a launch is 3.4 us).
 
-_types = None  # torch's types, by zs_dtype and zs_id_dtype
+_CODES = {C.c_int64: "q", C.c_int32: "i", C.c_double: "d", C.c_void_p: "P", C.c_size_t: "N"}
+_calls = {}  # name: (the struct's pack, the function on bytes)
+_types = {}  # torch's types: zs_dtype or zs_id_dtype
+
+
+def _load(name: str, args):
+    import torch
+
+    pack = struct.Struct("".join(_CODES[t] for _, t in args._fields_))
+    assert pack.size == C.sizeof(args)
+    lib()
+    _types.update({torch.float16: z.ZS_F16, torch.bfloat16: z.ZS_BF16, torch.float32: ZS_F32,
+                   torch.int32: ZS_I32, torch.int64: ZS_I64})
+    _calls[name] = pack.pack, C.CFUNCTYPE(C.c_int32, C.c_char_p)((name, z.lib()))
+    return _calls[name]
 
 
 def _type(x, given, names) -> int:
     """The type code of an operand: as given, or its tensor's."""
-    global _types
-    if given is not None or x is None or x.__class__ is int:
-        return _named(given, names)
-    if _types is None:
-        import torch
-
-        _types = {torch.float16: z.ZS_F16, torch.bfloat16: z.ZS_BF16, torch.float32: ZS_F32,
-                  torch.int32: ZS_I32, torch.int64: ZS_I64}
-    return _types.get(x.dtype, 0)
+    if given is None and x is not None and x.__class__ is not int:
+        return _types.get(x.dtype, 0)
+    return _named(given, names)
 
 
 def _rows(x, cols: int):
     """(address, stride) of rows of activations.  A tensor's last dimension is a
     row, and more than two dimensions are rows of one stride."""
-    if x is None or x.__class__ is int:
+    if x is None:
+        return 0, cols
+    if x.__class__ is int:
         return x, cols
     st = x.stride()
-    if len(st) < 2:
-        return x.data_ptr(), cols
-    if st[-1] != 1 and x.shape[-1] != 1:
-        raise ValueError("the elements of a row lie apart")
-    if len(st) > 2 and not x.is_contiguous():
+    if len(st) == 2:
+        stride, step = st
+        if step != 1 and x.shape[1] != 1:
+            raise ValueError("the elements of a row lie apart")
+        return x.data_ptr(), stride if stride >= cols or x.shape[0] > 1 else cols
+    if not x.is_contiguous():
         raise ValueError("rows of more than one stride")
-    return x.data_ptr(), st[-2] if x.shape[-2] > 1 or st[-2] > cols else cols
+    return x.data_ptr(), x.shape[-1] if len(st) > 2 else cols
 
 
 def _flat(x):
     """The address of an operand that has no strides."""
-    if x is None or x.__class__ is int:
+    if x is None:
+        return 0
+    if x.__class__ is int:
         return x
     if not x.is_contiguous():
         raise ValueError("a contiguous tensor expected")
     return x.data_ptr()
-
-
-def _done(st: int, where: str, check: bool) -> int:
-    if check and st:
-        z._check(st, where)
-    return st
 
 
 # ----------------------------------------------------------------- entry points
@@ -140,6 +150,7 @@ def zs_norm_forward(rows: int, cols: int, x, y, gamma=None, beta=None, *, kind="
                     stream=None, check=True) -> int:
     """kind: "layer" or "rms".  With a residual, total gets x + residual, and its norm goes to y.
     dtype: of x, residual, total and y; w_dtype: of gamma and beta; "f16", "bf16" or "f32"."""
+    pack, call = _calls.get("zs_norm_forward") or _load("zs_norm_forward", zs_norm_args)
     dt = _type(x, dtype, DTYPE_NAMES)
     w = gamma if gamma is not None else beta
     wdt = _type(w, w_dtype, DTYPE_NAMES) if w is not None else dt
@@ -147,9 +158,11 @@ def zs_norm_forward(rows: int, cols: int, x, y, gamma=None, beta=None, *, kind="
     pr, sr = _rows(residual, cols)
     pt, st_ = _rows(total, cols)
     py, sy = _rows(y, cols)
-    a = zs_norm_args(rows, cols, _named(kind, KINDS), dt, wdt, 0, eps, px, pr, pt, py, sx, sr, st_, sy,
-                     _flat(gamma), _flat(beta), _flat(mean), _flat(rstd), z._stream(stream))
-    return _done((_lib or lib()).zs_norm_forward(a), "zs_norm_forward", check)
+    st = call(pack(rows, cols, _named(kind, KINDS), dt, wdt, 0, eps, px, pr, pt, py, sx, sr, st_, sy,
+                   _flat(gamma), _flat(beta), _flat(mean), _flat(rstd), z._stream(stream) or 0))
+    if check:
+        z._check(st, "zs_norm_forward")
+    return st
 
 
 def zs_norm_workspace_bytes(rows: int, cols: int) -> int:
@@ -162,6 +175,7 @@ def zs_norm_backward(rows: int, cols: int, dy, x, rstd, dx, *, mean=None, gamma=
                      check=True) -> int:
     """x: what the forward pass normalised (its total where it had a residual), mean and rstd what
     it left.  dres: a gradient that is added to dx.  accumulate: dgamma and dbeta are added to."""
+    pack, call = _calls.get("zs_norm_backward") or _load("zs_norm_backward", zs_norm_grad_args)
     dt = _type(x, dtype, DTYPE_NAMES)
     wdt = _type(gamma, w_dtype, DTYPE_NAMES) if gamma is not None else dt
     g = dgamma if dgamma is not None else dbeta
@@ -170,10 +184,12 @@ def zs_norm_backward(rows: int, cols: int, dy, x, rstd, dx, *, mean=None, gamma=
     px, sx = _rows(x, cols)
     pr, sr = _rows(dres, cols)
     po, so = _rows(dx, cols)
-    a = zs_norm_grad_args(rows, cols, _named(kind, KINDS), dt, wdt, gdt, int(accumulate), 0, pd, px, pr,
-                          po, sd, sx, sr, so, _flat(gamma), _flat(mean), _flat(rstd), _flat(dgamma),
-                          _flat(dbeta), z._addr(workspace), ws_bytes, z._stream(stream))
-    return _done((_lib or lib()).zs_norm_backward(a), "zs_norm_backward", check)
+    st = call(pack(rows, cols, _named(kind, KINDS), dt, wdt, gdt, int(accumulate), 0, pd, px, pr, po, sd, sx,
+                   sr, so, _flat(gamma), _flat(mean), _flat(rstd), _flat(dgamma), _flat(dbeta),
+                   z._addr(workspace) or 0, ws_bytes, z._stream(stream) or 0))
+    if check:
+        z._check(st, "zs_norm_backward")
+    return st
 
 
 def zs_embed_forward(tokens: int, ids, rows: int, cols: int, table, y, *, scale=1.0, first_row=0,
@@ -181,12 +197,15 @@ def zs_embed_forward(tokens: int, ids, rows: int, cols: int, table, y, *, scale=
                      id_dtype=None, stream=None, check=True) -> int:
     """dtype: of y; table_dtype: of table and pos_table; id_dtype: of ids and pos_ids, "i32" or
     "i64".  Ids outside first_row .. first_row + rows - 1 give zeros."""
+    pack, call = _calls.get("zs_embed_forward") or _load("zs_embed_forward", zs_embed_args)
     py, sy = _rows(y, cols)
-    a = zs_embed_args(tokens, rows, cols, first_row, _type(ids, id_dtype, ID_NAMES),
-                      _type(y, dtype, DTYPE_NAMES), _type(table, table_dtype, DTYPE_NAMES), 0, scale,
-                      _flat(ids), _flat(table), py, sy, _flat(pos_ids), _flat(pos_table), pos_rows,
-                      z._stream(stream))
-    return _done((_lib or lib()).zs_embed_forward(a), "zs_embed_forward", check)
+    st = call(pack(tokens, rows, cols, first_row, _type(ids, id_dtype, ID_NAMES),
+                   _type(y, dtype, DTYPE_NAMES), _type(table, table_dtype, DTYPE_NAMES), 0, scale,
+                   _flat(ids), _flat(table), py, sy, _flat(pos_ids), _flat(pos_table), pos_rows,
+                   z._stream(stream) or 0))
+    if check:
+        z._check(st, "zs_embed_forward")
+    return st
 
 
 def zs_embed_workspace_bytes(tokens: int, rows: int, cols: int) -> int:
@@ -197,9 +216,12 @@ def zs_embed_backward(tokens: int, ids, rows: int, cols: int, dy, grad, workspac
                       scale=1.0, first_row=0, accumulate=False, dtype=None, grad_dtype=None,
                       id_dtype=None, stream=None, check=True) -> int:
     """accumulate: grad's rows that a token names are added to; else all of grad is written."""
+    pack, call = _calls.get("zs_embed_backward") or _load("zs_embed_backward", zs_embed_grad_args)
     pd, sd = _rows(dy, cols)
-    a = zs_embed_grad_args(tokens, rows, cols, first_row, _type(ids, id_dtype, ID_NAMES),
-                           _type(dy, dtype, DTYPE_NAMES), _type(grad, grad_dtype, DTYPE_NAMES),
-                           int(accumulate), scale, _flat(ids), pd, sd, _flat(grad),
-                           z._addr(workspace), ws_bytes, z._stream(stream))
-    return _done((_lib or lib()).zs_embed_backward(a), "zs_embed_backward", check)
+    st = call(pack(tokens, rows, cols, first_row, _type(ids, id_dtype, ID_NAMES),
+                   _type(dy, dtype, DTYPE_NAMES), _type(grad, grad_dtype, DTYPE_NAMES), int(accumulate),
+                   scale, _flat(ids), pd, sd, _flat(grad), z._addr(workspace) or 0, ws_bytes,
+                   z._stream(stream) or 0))
+    if check:
+        z._check(st, "zs_embed_backward")
+    return st

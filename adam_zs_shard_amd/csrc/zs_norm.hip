@@ -153,9 +153,11 @@ struct NormGradArgs {
   const void* gamma;
   const float* mean;
   const float* rstd;
-  float* partial;  // or null: no gradients of weights
+  float* partial;  // or null: no sums over rows here
+  void* dgamma;    // of the workgroups from `groups` on
+  void* dbeta;
   int64_t rows, beta_at;
-  int cols, wdt;
+  int cols, wdt, groups, gdt, accumulate;
 };
 
 template <int DT, int J>
@@ -192,8 +194,9 @@ __device__ __forceinline__ void forget(Pack<DT>& q) {
   }
 }
 
-// h = (x - mean) * rstd of a pack, zeros where the row has ended: 0 * rstd would
-// be NaN there if rstd is not finite.
+// h = (x - mean) * rstd of a pack, zeros where the row has ended within it.  Packs
+// wholly beyond the row (WHOLE) give values that only products with their dy, which
+// is 0, see.
 template <int DT, bool LAYER, bool WHOLE>
 __device__ __forceinline__ void normed(const Pack<DT>& x, float mean, float rstd, int left,
                                        float (&h)[kPack<DT>]) {
@@ -201,8 +204,70 @@ __device__ __forceinline__ void normed(const Pack<DT>& x, float mean, float rstd
 #pragma unroll
   for (int i = 0; i < kPack<DT>; ++i) {
     if constexpr (LAYER) h[i] = h[i] - mean;
-    h[i] = (WHOLE ? left > 0 : i < left) ? h[i] * rstd : 0.0f;
+    h[i] = WHOLE || i < left ? h[i] * rstd : 0.0f;
   }
+}
+
+// The weights' gradients of 8 packs of columns, straight from all rows: each 8 lanes
+// of the workgroup take a row at a time.
+constexpr int kColumnLanes = 8;
+
+template <int DT, int WG, bool LAYER, bool BETA, bool WHOLE>
+__device__ __forceinline__ void column_sums(const NormGradArgs& a, int slab) {
+  constexpr int V = kPack<DT>, kLoads = 4, kRows = WG / kColumnLanes;
+  __shared__ float sums[2][WG / kWave][kColumnLanes * V];
+  const int lane = threadIdx.x % kColumnLanes;
+  const int c = (slab * kColumnLanes + lane) * V, n = a.cols - c;
+  float acc_g[V], acc_b[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc_g[i] = acc_b[i] = 0.0f;
+  for (int64_t r = threadIdx.x / kColumnLanes; r < a.rows; r += kRows * kLoads) {
+    Pack<DT> dy[kLoads], x[kLoads];
+    float mean[kLoads], rstd[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int64_t q = r + u * kRows;
+      const int there = q < a.rows ? n : 0;
+      dy[u] = ld_some<DT, WHOLE, false>(reinterpret_cast<const char*>(a.dy.at + q * a.dy.pitch) + c * kSize<DT>, there);
+      x[u] = ld_some<DT, WHOLE, false>(reinterpret_cast<const char*>(a.x.at + q * a.x.pitch) + c * kSize<DT>, there);
+      mean[u] = LAYER && there > 0 ? a.mean[q] : 0.0f;
+      rstd[u] = there > 0 ? a.rstd[q] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      float h[V], t[V];
+      normed<DT, LAYER, WHOLE>(x[u], mean[u], rstd[u], r + u * kRows < a.rows ? n : 0, h);
+      widen<DT>(dy[u], t);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        acc_g[i] = __builtin_fmaf(t[i], h[i], acc_g[i]);
+        if constexpr (BETA) acc_b[i] += t[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int s = kColumnLanes; s < kWave; s *= 2) {
+      acc_g[i] += __shfl_xor(acc_g[i], s, kWave);
+      if constexpr (BETA) acc_b[i] += __shfl_xor(acc_b[i], s, kWave);
+    }
+  if (threadIdx.x % kWave < kColumnLanes) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      sums[0][threadIdx.x / kWave][lane * V + i] = acc_g[i];
+      if constexpr (BETA) sums[1][threadIdx.x / kWave][lane * V + i] = acc_b[i];
+    }
+  }
+  __syncthreads();
+  const int which = threadIdx.x / (kColumnLanes * V), k = threadIdx.x % (kColumnLanes * V);
+  const int64_t col = static_cast<int64_t>(slab) * kColumnLanes * V + k;
+  void* to = which == 0 ? a.dgamma : a.dbeta;
+  if (which > BETA || !to || col >= a.cols) return;
+  float s = sums[which][0][k];
+#pragma unroll
+  for (int w = 1; w < WG / kWave; ++w) s += sums[which][w][k];
+  st_value(to, a.gdt, col, a.accumulate ? ld_value(to, a.gdt, col) + s : s);
 }
 
 // A lane's sums go to place (j * V + i) * TEAM + lane of a row of sums, so that
@@ -211,6 +276,10 @@ __device__ __forceinline__ void normed(const Pack<DT>& x, float mean, float rstd
 template <int DT, int TEAM, int E, int WG, bool LAYER, bool BETA, bool WHOLE>
 __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
   constexpr int V = kPack<DT>, J = E / V, TEAMS = WG / TEAM;
+  if (static_cast<int>(blockIdx.x) >= a.groups) {
+    column_sums<DT, WG, LAYER, BETA, WHOLE>(a, static_cast<int>(blockIdx.x) - a.groups);
+    return;
+  }
   __shared__ float part[2][LAYER ? 2 : 1][16];
   extern __shared__ float sums[];  // WG * E, where there are several teams
   int turn = 0;
@@ -226,7 +295,7 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
     for (int i = 0; i < V; ++i) acc_g[j][i] = acc_b[j][i] = 0.0f;
   }
   const float n = static_cast<float>(a.cols);
-  const int64_t step = static_cast<int64_t>(gridDim.x) * TEAMS;
+  const int64_t step = static_cast<int64_t>(a.groups) * TEAMS;
   int64_t r = static_cast<int64_t>(blockIdx.x) * TEAMS + team;
   // every team of the workgroup makes as many turns as its first
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * TEAMS; r0 < a.rows; r0 += step, r += step) {
@@ -261,11 +330,14 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
     char* dx = reinterpret_cast<char*>(a.dx.at + r * a.dx.pitch);
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      // h and dy * gamma once more: to keep them would take 2 E registers
+      // h and dy * gamma once more; of 16 elements they are computed again, since to
+      // keep them would take registers that 16 waves per CU do not have
       const int c = (lane + j * TEAM) * V;
       float h[V], t[V];
-      forget(g.x[j]);
-      forget(g.dy[j]);
+      if constexpr (E > 8) {
+        forget(g.x[j]);
+        forget(g.dy[j]);
+      }
       normed<DT, LAYER, WHOLE>(g.x[j], g.mean, g.rstd, a.cols - c, h);
       widen<DT>(g.dy[j], t);
 #pragma unroll
@@ -377,6 +449,13 @@ constexpr int kNormHeld = 16384;
 // by the kernel before (32768 x 1024 bf16 22.4 us, read past it 27.4).
 constexpr int64_t kNormCached = int64_t{192} << 20;
 
+// The weights' gradients of few rows come from workgroups of the same launch that
+// read these rows again (8 lanes to a row, 64 or 128 rows at a time), not from rows
+// of sums and a second launch.  us in one launch / in two, layer norm, bf16: 333 x
+// 1001 7.2 / 9.1, 64 x 768 6.1 / 9.0, 1024 x 768 7.8 / 9.3, 2048 x 768 16.5 / 10.0,
+// 512 x 4096 8.3 / 14.5, 1024 x 4096 15.4 / 16.8, 256 x 16384 15.1 / 27.5.
+constexpr int64_t kNormFewRows = 1024, kNormFewElems = int64_t{1} << 22;
+
 constexpr int norm_group(int team) { return team == kWave ? 4 * kWave : team; }
 constexpr int grad_group(int team) { return team > 512 ? team : 512; }
 
@@ -427,7 +506,14 @@ hipError_t launch_norm_grad(const NormGradLaunch& L) {
   a.gamma = L.gamma;
   a.mean = L.mean;
   a.rstd = L.rstd;
-  a.partial = sums ? L.partial : nullptr;
+  // in place the rows' workgroups write what the columns' would read
+  const bool few = sums && L.rows <= kNormFewRows && L.rows * L.cols <= kNormFewElems &&
+                   L.dx.at != L.dy.at && L.dx.at != L.x.at;
+  a.partial = sums && !few ? L.partial : nullptr;
+  a.dgamma = L.dgamma;
+  a.dbeta = L.dbeta;
+  a.gdt = L.gdt;
+  a.accumulate = L.accumulate ? 1 : 0;
   a.rows = L.rows;
   a.cols = L.cols;
   a.wdt = L.wdt;
@@ -445,11 +531,15 @@ hipError_t launch_norm_grad(const NormGradLaunch& L) {
       j.width = decltype(e)::value * TEAM;
       a.beta_at = j.beta_at = static_cast<int64_t>(kNormParts) * j.width;
       if (j.parts == 0) return;
+      a.groups = j.parts;
+      constexpr int kSlab = kColumnLanes * kPack<decltype(d)::value>;
+      const int columns = few ? (L.cols + kSlab - 1) / kSlab : 0;
+      const dim3 grid(static_cast<unsigned>(a.groups + columns));
       const size_t lds = TEAMS > 1 ? sizeof(float) * decltype(e)::value * WG : 0;
       const auto go = [&](auto layer, auto beta, auto whole) {
         norm_grad_kernel<decltype(d)::value, TEAM, decltype(e)::value, WG, decltype(layer)::value != 0,
                          decltype(beta)::value != 0, decltype(whole)::value != 0>
-            <<<dim3(static_cast<unsigned>(j.parts)), WG, lds, L.stream>>>(a);
+            <<<grid, WG, lds, L.stream>>>(a);
       };
       const auto pick = [&](auto whole) {
         L.layer ? go(IC<1>{}, IC<1>{}, whole) : L.dbeta ? go(IC<0>{}, IC<1>{}, whole) : go(IC<0>{}, IC<0>{}, whole);
@@ -459,7 +549,7 @@ hipError_t launch_norm_grad(const NormGradLaunch& L) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (!sums) return hipSuccess;
+  if (!sums || few) return hipSuccess;
   j.partial = L.partial;
   j.dgamma = L.dgamma;
   j.dbeta = L.dbeta;

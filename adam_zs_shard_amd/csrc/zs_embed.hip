@@ -458,20 +458,64 @@ struct SumArgs {
 };
 
 
+// V columns of a row of the gradient as they are held, so that several rows' take
+// few registers while they are in flight.
+template <int V, int GDT>
+struct Held {
+  uint32_t x[V * kSize<GDT> / 4];
+};
+template <int V, int GDT>
+__device__ __forceinline__ Held<V, GDT> ld_held(const char* at, int n) {
+  Held<V, GDT> h{};
+  constexpr int N = V * kSize<GDT> / 4;
+  if (n >= V) {
+    if constexpr (N == 2) {
+      const u32x2 q = *reinterpret_cast<const u32x2*>(at);
+      h.x[0] = q[0];
+      h.x[1] = q[1];
+    } else {
+#pragma unroll
+      for (int k = 0; k < N / 4; ++k) {
+        const u32x4 q = reinterpret_cast<const u32x4*>(at)[k];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h.x[4 * k + i] = q[i];
+      }
+    }
+  } else if (n > 0) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) {
+        if constexpr (GDT == kF32)
+          h.x[i] = reinterpret_cast<const uint32_t*>(at)[i];
+        else
+          h.x[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[i]) << (16 * (i % 2));
+      }
+  }
+  return h;
+}
+template <int V, int GDT>
+__device__ __forceinline__ float held(const Held<V, GDT>& h, int i) {
+  if constexpr (GDT == kF32) return __builtin_bit_cast(float, h.x[i]);
+  else return i % 2 == 0 ? widen_lo<GDT>(h.x[i / 2]) : widen_hi<GDT>(h.x[i / 2]);
+}
+
 // V columns of a row of the gradient, n of them there; old: what it holds.
 template <int V, int GDT, bool ADD>
 __device__ __forceinline__ void st_grad(const SumArgs& a, int64_t row, int c, int n, const Vals<V>& sum,
-                                        const Vals<V>& old) {
+                                        const Held<V, GDT>& old) {
   Vals<V> f;
 #pragma unroll
-  for (int i = 0; i < V; ++i) f.v[i] = ADD ? old.v[i] + sum.v[i] * a.scale : sum.v[i] * a.scale;
+  for (int i = 0; i < V; ++i) {
+    f.v[i] = sum.v[i] * a.scale;
+    if constexpr (ADD) f.v[i] = held<V, GDT>(old, i) + f.v[i];
+  }
   st_vals<V, GDT>(static_cast<char*>(a.grad) + (row * a.cols + c) * kSize<GDT>, n, f);
 }
 template <int V, int GDT, bool ADD>
-__device__ __forceinline__ Vals<V> ld_grad(const SumArgs& a, int64_t row, int c, int n) {
+__device__ __forceinline__ Held<V, GDT> ld_grad(const SumArgs& a, int64_t row, int c, int n) {
   if constexpr (ADD)
-    if (n > 0) return ld_vals<V, GDT>(static_cast<const char*>(a.grad) + (row * a.cols + c) * kSize<GDT>, n, 0.0f);
-  return Vals<V>{};
+    return ld_held<V, GDT>(static_cast<const char*>(a.grad) + (row * a.cols + c) * kSize<GDT>, n);
+  return Held<V, GDT>{};
 }
 
 // V sums, n of them there, through the cache: the next kernel reads them.
@@ -579,10 +623,10 @@ __device__ __forceinline__ void sum_unit(const SumArgs& a, int64_t unit) {
 #pragma unroll
   for (int i = 0; i < V; ++i) sum.v[i] = 0.0f;
   // rows of dy in flight per wave, and of the gradient that are added to
-  constexpr int kLoads = ADD && GDT == kF32 && V == 8 ? 4 : 8;
+  constexpr int kLoads = 8;
   for (; l < end; l += kLoads) {
     Pack<DT> p[kLoads];
-    Vals<V> old[kLoads];
+    Held<V, GDT> old[kLoads];
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       if (l + u >= end) break;
@@ -636,7 +680,7 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void sum_join_kernel(SumArgs a)
     const int64_t k = unit / a.slabs, w = a.long_rows[1 + k];
     const int c = (static_cast<int>(unit - k * a.slabs) * kWave + lane) * kJoinV, n = a.cols - c;
     const uint32_t row = a.list[(w + 1) * W].row;
-    Vals<kJoinV> old{};
+    Held<kJoinV, GDT> old{};
     if (wave == 0) old = ld_grad<kJoinV, GDT, ADD>(a, row, c, n);
     int64_t more = 1;  // windows after w that it meets
     // of the next 64, or of each 64th, those up to the first that it does not meet

@@ -17,8 +17,8 @@
  * once (correctly rounded division and root); only a product that goes straight
  * into a sum over a row or over rows is not rounded before it is added.  Such
  * sums are in an order that is fixed by the call's sizes, whether it is in
- * place, and the device: the same bits every time.  Infinities and NaN propagate by IEEE rules, within
- * their row and into the gradients' sums.
+ * place, and the device: the same bits every time.  Infinities and NaN
+ * propagate by IEEE rules, within their row and into the gradients' sums.
  *
  * Rows of activations are row-major with a stride in elements, at least cols;
  * what lies between two rows is neither read nor written.  Element types are

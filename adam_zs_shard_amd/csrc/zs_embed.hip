@@ -1,14 +1,24 @@
 // zs_embed.hip -- lookup in an embedding table, and the table's gradient.
 //
-// The lookup copies rows: each lane takes 16 bytes of a token's row.  The
-// gradient is a sum over the tokens that name a row, without atomics so that its
-// order is fixed: the tokens are sorted by row (a stable radix sort, so that
-// equal rows keep the tokens' order), the sorted list is cut into chunks, and a
-// wave sums the rows of dy of one chunk and 1 KiB of columns.  A table's row
-// whose tokens all lie in one chunk is written at once; the others' sums go to
-// the workspace, and a last kernel adds them in their order.  The pass over dy
-// and the table's gradient bounds it; with accumulate = 0 the table is cleared by
-// the workgroups that the sort leaves free.
+// The lookup copies rows, a lane 16 bytes of a token's.  HBM bounds it where the
+// tokens are many (16384 of 4096 bf16 columns 34 us, 5.4 TB/s), latency where they
+// are few: each row's address waits for the token's id.
+//
+// The gradient's row r is the sum of the rows of dy whose tokens name r, in the
+// tokens' order and without atomics, so that it has the same bits every time.  The
+// tokens are sorted by row, stably (one launch, or two per digit of the row for many
+// tokens); the sorted list is cut into windows, and a wave sums the rows of dy of one
+// window and 1 KiB of columns.  A table row with more tokens than a window has
+// places is summed in parts, which go to the workspace, and a last kernel adds them
+// in their order.  With accumulate = 0 the table is cleared by the launch that
+// sorts, beside it; so the rows that tokens name are written twice, 45 MB of the 1.1
+// GB that 16384 tokens of a 128256 x 4096 table move, for 20 us of sorting that
+// nothing waits for.
+//
+// HBM bounds large tables and many tokens: 16384 tokens, 128256 x 4096 bf16: 165 us
+// of clearing at 6.4 TB/s, 42 of sums at 4.7, 6 of parts.  131072 tokens added to
+// 16032 x 1024 fp32: 23 us of sorting, 66 of sums at 5.4 TB/s, 17 of parts.  Few
+// tokens wait: 500 added to 50257 x 768 4.4, 6 and 3.5 us for a MB or two.
 
 #include "zs_layer_device.h"
 
@@ -186,6 +196,9 @@ __device__ __forceinline__ uint32_t scan_lanes(uint32_t mine, uint32_t* work, ui
 // the counts into the places of each wave's tokens.
 constexpr int kBuckets = 64;
 constexpr int kFew = 512;    // tokens that are sorted by comparison at most
+// Where all workgroups go through all tokens, their time grows with these: 2048, 4096,
+// 8192 and 16384 tokens 6, 8.5, 11.5 and 19 us; 131072 97, where the passes below
+// take 25.
 constexpr int kIdSteps = 8;  // steps of 64 tokens whose ids a wave loads together
 
 // A wave's run of the tokens; the rows of its first kIdSteps steps stay in registers.
@@ -227,7 +240,7 @@ __global__ __launch_bounds__(LANES) void sort_buckets_kernel(SortArgs a) {
   __shared__ u32x4a16 keys[kFew / 4];
   if (blockIdx.x >= kBuckets) {
     clear_part<LANES>(a.clear, a.clear_bytes, static_cast<int64_t>(blockIdx.x) - kBuckets,
-                           gridDim.x - kBuckets);
+                      gridDim.x - kBuckets);
     return;
   }
   const uint32_t bucket = blockIdx.x, none = static_cast<uint32_t>(a.rows);
@@ -347,14 +360,17 @@ __global__ __launch_bounds__(LANES) void sort_buckets_kernel(SortArgs a) {
 }
 static_assert(1 << kBucketBits <= 512 && kFew <= 512, "a digit or a token per lane");
 
-// More tokens, several launches: each workgroup has a tile of the tokens, and each of its waves a run of
-// the tile.  Two kernels per pass: one counts the tiles' digits, the other adds up
-// the counts before its tile and digit and puts the tokens in their places.
+// More tokens, several launches: each workgroup has a tile of the tokens, and each of
+// its waves a run of the tile.  Two kernels per pass: one counts the tiles' digits,
+// the other adds up the counts before its tile and digit and puts the tokens in
+// their places.  Short tiles, so that many waves wait at once: all of the gradient
+// of 131072 tokens 107 us with tiles of 1024, 108 with 2048, 117 with 4096; of
+// 32768 49, 53 and 65.
 constexpr int kTileLanes = 512, kTileWaves = kTileLanes / kWave;
 constexpr int kTileSteps = 2;  // of 64 tokens, that a wave loads together
 
-// Calls f(step's first token, K tokens' rows and numbers, how many of the lane's
-// are there) over a wave's run of the tile.
+// Calls f(row and token, whether they are there) for the steps of a wave's run of the
+// tile.
 template <bool WIDE, bool FIRST, class F>
 __device__ __forceinline__ void for_run(const SortArgs& a, const TokenRow* from, F&& f) {
   constexpr int K = kTileSteps;
@@ -456,7 +472,6 @@ struct SumArgs {
   int cols, slabs;      // slabs: of a wave's columns
   float scale;
 };
-
 
 // V columns of a row of the gradient as they are held, so that several rows' take
 // few registers while they are in flight.
@@ -667,7 +682,11 @@ __global__ __launch_bounds__(kBlock) void sum_kernel(SumArgs a) {
 }
 
 // A long row's sum: a workgroup per row and 256 columns, whose waves take equal
-// shares of its windows' sums.
+// shares of its windows' sums.  131072 tokens of 1024 columns, 6e2 long rows, the
+// longest of 490 windows: 17 us, of which 37 MB of sums are a third; the rest is a
+// chain of five dependent loads per row.  Four waves 22 us, sixteen 26; a wave to a
+// row of at most 16 windows, and a workgroup to others, 16 here and 8 for 5 with
+// 8192 tokens.
 constexpr int kJoinV = 4, kJoinSlab = kWave * kJoinV, kJoinLoads = 8, kJoinWaves = 8;
 
 template <int W, int GDT, bool ADD>
@@ -720,7 +739,6 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void sum_join_kernel(SumArgs a)
     sums[wave][lane] = sum;
     __syncthreads();
     if (wave == 0) {
-
 #pragma unroll
       for (int i = 1; i < kJoinWaves; ++i)
 #pragma unroll

@@ -72,17 +72,14 @@ class Operands {
         const Span &w = spans_[i], &s = spans_[j];
         if (i == j || !w.written) continue;
         const bool same = w.lo == s.lo && w.hi == s.hi && w.pitch == s.pitch && w.width == s.width;
-        if (in_place && same && !s.written && s.width == row_bytes_ && i < in_place_most_) continue;
+        if (in_place && same && !s.written && i < rows_ && j < rows_) continue;
         if (clash(w, s)) return ZS_ERR_ALIAS;
       }
     return ZS_OK;
   }
   // The operands given so far are rows of activations, which outputs among them
   // may share with inputs among them.
-  void end_of_rows(int64_t row_bytes) {
-    row_bytes_ = row_bytes;
-    in_place_most_ = count_;
-  }
+  void end_of_rows() { rows_ = count_; }
 
  private:
   void fail(zs_status s) { status_ = s; }
@@ -91,8 +88,7 @@ class Operands {
     return meet(a, b);
   }
   Span spans_[16];
-  int count_ = 0, in_place_most_ = 0;
-  int64_t row_bytes_ = -1;
+  int count_ = 0, rows_ = 0;
   zs_status status_ = ZS_OK;
 };
 
@@ -127,7 +123,7 @@ zs_status norm_forward(const zs_norm_args* q) {
     o.rows(q->total, q->rows, q->cols, q->total_stride, size, true, &L.total);
   }
   o.rows(q->y, q->rows, q->cols, q->y_stride, size, true, &L.y);
-  o.end_of_rows(q->cols * size);
+  o.end_of_rows();
   if (q->gamma) o.vector(q->gamma, q->cols, wsize, false);
   if (q->beta) o.vector(q->beta, q->cols, wsize, false);
   if (layer && q->mean) o.vector(q->mean, q->rows, 4, true);
@@ -161,7 +157,7 @@ zs_status norm_backward(const zs_norm_grad_args* q) {
   o.rows(q->x, q->rows, q->cols, q->x_stride, size, false, &L.x);
   if (q->dres) o.rows(q->dres, q->rows, q->cols, q->dres_stride, size, false, &L.dres);
   o.rows(q->dx, q->rows, q->cols, q->dx_stride, size, true, &L.dx);
-  o.end_of_rows(q->cols * size);
+  o.end_of_rows();
   if (q->gamma) o.vector(q->gamma, q->cols, size_of(q->w_dtype), false);
   if (q->rows > 0) {
     if (layer) o.vector(q->mean, q->rows, 4, false);

@@ -479,7 +479,7 @@ hipError_t launch_norm(const NormLaunch& L) {
   with_shape<16>(L.dt, L.cols, [&](auto d, auto team, auto e) {
     constexpr int TEAM = decltype(team)::value, WG = norm_group(TEAM), TEAMS = WG / TEAM;
     const int64_t groups = (L.rows + TEAMS - 1) / TEAMS;
-    const int64_t most = L.residual.at && TEAM < 1024 ? kMaxGroups
+    const int64_t most = L.residual.at && TEAM < 1024 ? kMaxGroups / (WG > kBlock ? WG / kBlock : 1)
                                                      : int64_t{cu_count()} * (kNormHeld / decltype(e)::value / WG);
     const dim3 grid(static_cast<unsigned>(groups < most ? groups : most));
     const auto go = [&](auto layer, auto whole, auto past) {

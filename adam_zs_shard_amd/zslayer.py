@@ -93,6 +93,7 @@ def lib():
 _CODES = {C.c_int64: "q", C.c_int32: "i", C.c_double: "d", C.c_void_p: "P", C.c_size_t: "N"}
 _calls = {}  # name: (the struct's pack, the function on bytes)
 _types = {}  # torch's types: zs_dtype or zs_id_dtype
+_torch = {}  # and back
 
 
 def _load(name: str, args):
@@ -103,6 +104,7 @@ def _load(name: str, args):
     lib()
     _types.update({torch.float16: z.ZS_F16, torch.bfloat16: z.ZS_BF16, torch.float32: ZS_F32,
                    torch.int32: ZS_I32, torch.int64: ZS_I64})
+    _torch.update({code: t for t, code in _types.items()})
     _calls[name] = pack.pack, C.CFUNCTYPE(C.c_int32, C.c_char_p)((name, z.lib()))
     return _calls[name]
 
@@ -114,13 +116,15 @@ def _type(x, given, names) -> int:
     return _named(given, names)
 
 
-def _rows(x, cols: int):
-    """(address, stride) of rows of activations.  A tensor's last dimension is a
-    row, and more than two dimensions are rows of one stride."""
+def _rows(x, cols: int, dtype):
+    """(address, stride) of rows of activations of torch's dtype.  A tensor's last dimension
+    is a row, and more than two dimensions are rows of one stride."""
     if x is None:
         return 0, cols
     if x.__class__ is int:
         return x, cols
+    if x.dtype is not dtype:
+        raise ValueError(f"{x.dtype}, {dtype} expected")
     st = x.stride()
     if len(st) == 2:
         stride, step = st
@@ -132,12 +136,14 @@ def _rows(x, cols: int):
     return x.data_ptr(), x.shape[-1] if len(st) > 2 else cols
 
 
-def _flat(x):
-    """The address of an operand that has no strides."""
+def _flat(x, dtype):
+    """The address of an operand of torch's dtype that has no strides."""
     if x is None:
         return 0
     if x.__class__ is int:
         return x
+    if x.dtype is not dtype:
+        raise ValueError(f"{x.dtype}, {dtype} expected")
     if not x.is_contiguous():
         raise ValueError("a contiguous tensor expected")
     return x.data_ptr()
@@ -154,12 +160,14 @@ def zs_norm_forward(rows: int, cols: int, x, y, gamma=None, beta=None, *, kind="
     dt = _type(x, dtype, DTYPE_NAMES)
     w = gamma if gamma is not None else beta
     wdt = _type(w, w_dtype, DTYPE_NAMES) if w is not None else dt
-    px, sx = _rows(x, cols)
-    pr, sr = _rows(residual, cols)
-    pt, st_ = _rows(total, cols)
-    py, sy = _rows(y, cols)
+    t, tw, f32 = _torch.get(dt), _torch.get(wdt), _torch[ZS_F32]
+    px, sx = _rows(x, cols, t)
+    pr, sr = _rows(residual, cols, t)
+    pt, st_ = _rows(total, cols, t)
+    py, sy = _rows(y, cols, t)
     st = call(pack(rows, cols, _named(kind, KINDS), dt, wdt, 0, eps, px, pr, pt, py, sx, sr, st_, sy,
-                   _flat(gamma), _flat(beta), _flat(mean), _flat(rstd), z._stream(stream) or 0))
+                   _flat(gamma, tw), _flat(beta, tw), _flat(mean, f32), _flat(rstd, f32),
+                   z._stream(stream) or 0))
     if check:
         z._check(st, "zs_norm_forward")
     return st
@@ -180,13 +188,15 @@ def zs_norm_backward(rows: int, cols: int, dy, x, rstd, dx, *, mean=None, gamma=
     wdt = _type(gamma, w_dtype, DTYPE_NAMES) if gamma is not None else dt
     g = dgamma if dgamma is not None else dbeta
     gdt = _type(g, grad_dtype, DTYPE_NAMES) if g is not None else dt
-    pd, sd = _rows(dy, cols)
-    px, sx = _rows(x, cols)
-    pr, sr = _rows(dres, cols)
-    po, so = _rows(dx, cols)
+    t, tg, f32 = _torch.get(dt), _torch.get(gdt), _torch[ZS_F32]
+    pd, sd = _rows(dy, cols, t)
+    px, sx = _rows(x, cols, t)
+    pr, sr = _rows(dres, cols, t)
+    po, so = _rows(dx, cols, t)
     st = call(pack(rows, cols, _named(kind, KINDS), dt, wdt, gdt, int(accumulate), 0, pd, px, pr, po, sd, sx,
-                   sr, so, _flat(gamma), _flat(mean), _flat(rstd), _flat(dgamma), _flat(dbeta),
-                   z._addr(workspace) or 0, ws_bytes, z._stream(stream) or 0))
+                   sr, so, _flat(gamma, _torch.get(wdt)), _flat(mean, f32), _flat(rstd, f32),
+                   _flat(dgamma, tg), _flat(dbeta, tg), z._addr(workspace) or 0, ws_bytes,
+                   z._stream(stream) or 0))
     if check:
         z._check(st, "zs_norm_backward")
     return st
@@ -198,10 +208,12 @@ def zs_embed_forward(tokens: int, ids, rows: int, cols: int, table, y, *, scale=
     """dtype: of y; table_dtype: of table and pos_table; id_dtype: of ids and pos_ids, "i32" or
     "i64".  Ids outside first_row .. first_row + rows - 1 give zeros."""
     pack, call = _calls.get("zs_embed_forward") or _load("zs_embed_forward", zs_embed_args)
-    py, sy = _rows(y, cols)
-    st = call(pack(tokens, rows, cols, first_row, _type(ids, id_dtype, ID_NAMES),
-                   _type(y, dtype, DTYPE_NAMES), _type(table, table_dtype, DTYPE_NAMES), 0, scale,
-                   _flat(ids), _flat(table), py, sy, _flat(pos_ids), _flat(pos_table), pos_rows,
+    dt, tdt, idt = (_type(y, dtype, DTYPE_NAMES), _type(table, table_dtype, DTYPE_NAMES),
+                    _type(ids, id_dtype, ID_NAMES))
+    ti, tt = _torch.get(idt), _torch.get(tdt)
+    py, sy = _rows(y, cols, _torch.get(dt))
+    st = call(pack(tokens, rows, cols, first_row, idt, dt, tdt, 0, scale, _flat(ids, ti),
+                   _flat(table, tt), py, sy, _flat(pos_ids, ti), _flat(pos_table, tt), pos_rows,
                    z._stream(stream) or 0))
     if check:
         z._check(st, "zs_embed_forward")
@@ -217,11 +229,12 @@ def zs_embed_backward(tokens: int, ids, rows: int, cols: int, dy, grad, workspac
                       id_dtype=None, stream=None, check=True) -> int:
     """accumulate: grad's rows that a token names are added to; else all of grad is written."""
     pack, call = _calls.get("zs_embed_backward") or _load("zs_embed_backward", zs_embed_grad_args)
-    pd, sd = _rows(dy, cols)
-    st = call(pack(tokens, rows, cols, first_row, _type(ids, id_dtype, ID_NAMES),
-                   _type(dy, dtype, DTYPE_NAMES), _type(grad, grad_dtype, DTYPE_NAMES), int(accumulate),
-                   scale, _flat(ids), pd, sd, _flat(grad), z._addr(workspace) or 0, ws_bytes,
-                   z._stream(stream) or 0))
+    dt, gdt, idt = (_type(dy, dtype, DTYPE_NAMES), _type(grad, grad_dtype, DTYPE_NAMES),
+                    _type(ids, id_dtype, ID_NAMES))
+    pd, sd = _rows(dy, cols, _torch.get(dt))
+    st = call(pack(tokens, rows, cols, first_row, idt, dt, gdt, int(accumulate), scale,
+                   _flat(ids, _torch.get(idt)), pd, sd, _flat(grad, _torch.get(gdt)),
+                   z._addr(workspace) or 0, ws_bytes, z._stream(stream) or 0))
     if check:
         z._check(st, "zs_embed_backward")
     return st

@@ -93,6 +93,7 @@ def test_norm_refuses_overlap():
     for over in (dict(y=at(0) + size - 2), dict(total=at(1) + 2), dict(y=at(2) - size + 2), dict(y=at(3)),
                  dict(mean=at(0) + 4), dict(rstd=at(6) + 12), dict(mean=at(1) + size - 4), dict(rstd=at(2)),
                  dict(y=at(5)),                   # both outputs
+                 dict(rows=1, y=at(2)),           # of one row: as large as a weight
                  dict(y=at(0) + 200),             # one row on
                  dict(y=at(4) + 2)):
         assert norm(**over) == z.ZS_ERR_ALIAS, over
@@ -237,9 +238,21 @@ def test_binding_refuses_tensors_that_it_cannot_name():
         a.zs_embed_forward(4, torch.zeros(8, dtype=torch.int64)[::2], 4, 20, x, x)
     with pytest.raises(ValueError):
         a.zs_norm_forward(4, 10, torch.zeros(2, 2, 20)[:, :, :10], x)
-    assert a._rows(x[:, :10], 10) == (x.data_ptr(), 20)
-    assert a._rows(x[:1], 20) == (x.data_ptr(), 20)
-    assert a._rows(torch.zeros(2, 3, 7), 7)[1] == 7
+    assert a._rows(x[:, :10], 10, x.dtype) == (x.data_ptr(), 20)
+    assert a._rows(x[:1], 20, x.dtype) == (x.data_ptr(), 20)
+    assert a._rows(torch.zeros(2, 3, 7), 7, torch.float32)[1] == 7
+    # types that do not go together
+    f, w, i = torch.zeros(4, 20), torch.zeros(20), torch.zeros(4, dtype=torch.int64)
+    for call in (lambda: a.zs_norm_forward(4, 20, x, f), lambda: a.zs_norm_forward(4, 20, f, x),
+                 lambda: a.zs_norm_forward(4, 20, f, f, w, w.half()),
+                 lambda: a.zs_norm_forward(4, 20, x, x.clone(), rstd=x[0]),
+                 lambda: a.zs_norm_backward(4, 20, f, x, w, x),
+                 lambda: a.zs_norm_backward(4, 20, f, f, w, f, dgamma=w, dbeta=x[0]),
+                 lambda: a.zs_embed_forward(4, i, 4, 20, x, f, pos_ids=i.int(), pos_rows=4, pos_table=x),
+                 lambda: a.zs_embed_forward(4, i, 4, 20, x, f, pos_ids=i, pos_rows=4, pos_table=f),
+                 lambda: a.zs_embed_backward(4, i, 4, 20, f.double(), f, f, 0)):
+        with pytest.raises((ValueError, z.ZsError)):
+            call()
 
 
 # ----------------------------------------------------------------- the references

@@ -27,9 +27,10 @@ DEVICE = [f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "-Xclang", "-p
 
 # Device code is split over several translation units (the fused kernels per
 # gradient dtype) so that they compile in parallel.
-SOURCES = ["zs_fused_f16.hip", "zs_fused_bf16.hip", "zs_table.hip", "zs_unfused.hip",
+# The ones that take longest come first.
+SOURCES = ["zs_embed.hip", "zs_norm_grad.hip", "zs_norm.hip",
+           "zs_fused_f16.hip", "zs_fused_bf16.hip", "zs_table.hip", "zs_unfused.hip",
            "zs_common.hip", "zs_adamw32.hip", "zs_adamw8.hip", "zs_adamw_norm.hip",
-           "zs_norm.hip", "zs_embed.hip",
            "zs_capi.cpp", "zs_offload.cpp", "zs_adamw.cpp", "zs_layer.cpp"]
 # Host-only code (the CPU offload update), compiled as plain C++: SIMD code
 # paths are selected per function with target attributes.

@@ -129,7 +129,8 @@ __device__ __forceinline__ void clear_part(char* at, int64_t bytes, int64_t i, i
 }
 // As many as the bytes need; fewer where a launch cannot count them.
 int64_t clear_groups(int64_t bytes, int lanes) {
-  const int64_t groups = (bytes + 15 + 16 * lanes - 1) / (16 * lanes), most = kMaxGroups / (lanes / kBlock) - 4096;
+  const int64_t groups = (bytes + 15 + 16 * lanes - 1) / (16 * lanes);
+  const int64_t most = kMaxGroups / (lanes / kBlock) - 4096;
   return groups < most ? groups : most;
 }
 
@@ -397,10 +398,11 @@ __device__ __forceinline__ void for_run(const SortArgs& a, const TokenRow* from,
 }
 
 template <bool WIDE, bool FIRST>
-__global__ __launch_bounds__(kTileLanes) void sort_count_kernel(SortArgs a, const TokenRow* from, int shift,
-                                                           int tiles) {
+__global__ __launch_bounds__(kTileLanes) void sort_count_kernel(SortArgs a, const TokenRow* from,
+                                                               int shift, int tiles) {
   if (static_cast<int>(blockIdx.x) >= tiles) {
-    clear_part<kTileLanes>(a.clear, a.clear_bytes, static_cast<int64_t>(blockIdx.x) - tiles, gridDim.x - tiles);
+    clear_part<kTileLanes>(a.clear, a.clear_bytes, static_cast<int64_t>(blockIdx.x) - tiles,
+                           gridDim.x - tiles);
     return;
   }
   __shared__ uint32_t counts[1 << kSortBits];
@@ -416,8 +418,8 @@ __global__ __launch_bounds__(kTileLanes) void sort_count_kernel(SortArgs a, cons
 }
 
 template <bool WIDE, bool FIRST>
-__global__ __launch_bounds__(kTileLanes) void sort_place_kernel(SortArgs a, const TokenRow* from, TokenRow* to,
-                                                           int shift) {
+__global__ __launch_bounds__(kTileLanes) void sort_place_kernel(SortArgs a, const TokenRow* from,
+                                                               TokenRow* to, int shift) {
   __shared__ uint32_t counts[kTileWaves << kSortBits];
   __shared__ uint32_t work[kTileWaves];
   const int digits = 1 << a.bits;
@@ -539,7 +541,8 @@ __device__ __forceinline__ void st_sums(float* to, int n, const Vals<V>& x) {
 #pragma unroll
   for (int k = 0; k < V / 4; ++k) {
     if (n >= 4 * k + 4) {
-      *reinterpret_cast<f32x4*>(to + 4 * k) = f32x4{x.v[4 * k], x.v[4 * k + 1], x.v[4 * k + 2], x.v[4 * k + 3]};
+      *reinterpret_cast<f32x4*>(to + 4 * k) =
+          f32x4{x.v[4 * k], x.v[4 * k + 1], x.v[4 * k + 2], x.v[4 * k + 3]};
     } else {
 #pragma unroll
       for (int i = 4 * k; i < 4 * k + 4; ++i)
@@ -771,7 +774,8 @@ EmbedLayout embed_layout(int64_t tokens, int64_t cols) {
   EmbedLayout l;
   const size_t list = up256(sizeof(TokenRow) * static_cast<size_t>(tokens));
   const size_t windows = static_cast<size_t>((tokens - 1) / window_of(tokens, cols) + 1);
-  const size_t tiles = tokens <= kSortAlone ? 0 : static_cast<size_t>((tokens + tile_of(tokens) - 1) / tile_of(tokens));
+  const size_t tiles =
+      tokens <= kSortAlone ? 0 : static_cast<size_t>((tokens - 1) / tile_of(tokens) + 1);
   l.list = 0;
   l.other = list;
   l.counts = l.other + list;
@@ -841,7 +845,8 @@ hipError_t launch_sort(const EmbedGradLaunch& L, const EmbedLayout& lay) {
     digits(bits_of(static_cast<uint64_t>(L.rows - 1) / kBuckets), kBucketBits);
     const auto go = [&](auto lanes) {
       constexpr int LANES = decltype(lanes)::value;
-      const dim3 grid(static_cast<unsigned>(kBuckets + (L.accumulate ? 0 : clear_groups(a.clear_bytes, LANES))));
+      const int64_t clearers = L.accumulate ? 0 : clear_groups(a.clear_bytes, LANES);
+      const dim3 grid(static_cast<unsigned>(kBuckets + clearers));
       if (L.wide_ids) sort_buckets_kernel<true, LANES><<<grid, LANES, 0, L.stream>>>(a);
       else sort_buckets_kernel<false, LANES><<<grid, LANES, 0, L.stream>>>(a);
     };
@@ -911,14 +916,15 @@ hipError_t launch_embed_grad(const EmbedGradLaunch& L) {
         constexpr int DT = decltype(d)::value, kSlab = kWave * kPack<DT>;
         a.slabs = (L.cols + kSlab - 1) / kSlab;
         const int64_t groups = (static_cast<int64_t>(a.windows) * a.slabs + kWaves - 1) / kWaves;
-        sum_kernel<W, DT, GDT, ADD><<<dim3(static_cast<unsigned>(groups < kMaxGroups ? groups : kMaxGroups)), kBlock,
-                                   0, L.stream>>>(a);
+        const dim3 grid(static_cast<unsigned>(groups < kMaxGroups ? groups : kMaxGroups));
+        sum_kernel<W, DT, GDT, ADD><<<grid, kBlock, 0, L.stream>>>(a);
       });
       if (L.tokens <= W) return;  // no long row
       a.slabs = (L.cols + kJoinSlab - 1) / kJoinSlab;
       const int64_t most = int64_t{cu_count()} * (32 / kJoinWaves);
       const int64_t units = L.tokens / (W + 1) * a.slabs;
-      sum_join_kernel<W, GDT, ADD><<<dim3(static_cast<unsigned>(units < most ? units : most)), kJoinWaves * kWave, 0, L.stream>>>(a);
+      const dim3 grid(static_cast<unsigned>(units < most ? units : most));
+      sum_join_kernel<W, GDT, ADD><<<grid, kJoinWaves * kWave, 0, L.stream>>>(a);
     };
     const auto pick = [&](auto w) { L.accumulate ? go(IC<1>{}, w) : go(IC<0>{}, w); };
     window == kWindowFew ? pick(IC<kWindowFew>{}) : pick(IC<kWindowMany>{});

@@ -289,9 +289,26 @@ def test_norm_grad_of_what_is_wanted(kind, want):
 
 
 @pytest.mark.parametrize("place", ["dx=dy", "dx=x", "dx=dres"])
-@pytest.mark.parametrize("cols", [100, 768, 6000])
-def test_norm_grad_in_place(place, cols):
-    run_norm_grad(2500, cols, "layer", "bf16", dres=True, place=place)
+@pytest.mark.parametrize("rows,cols", [(2500, 100), (2500, 768), (2500, 6000), (400, 768), (90, 5000), (1, 31)])
+def test_norm_grad_in_place(place, rows, cols):
+    run_norm_grad(rows, cols, "layer", "bf16", dres=True, place=place)
+
+
+def test_norm_grad_of_columns_of_one_buffer():
+    """dy, x and dx side by side in the same rows, few enough to be read twice."""
+    g = gen(4)
+    b = torch.randn(300, 3 * 256, generator=g).bfloat16().to(DEV)
+    dy, x, dx = b[:, :256], b[:, 256:512], b[:, 512:]
+    keep = b[:, :512].clone()
+    rstd, dg = torch.rand(300, generator=g).to(DEV), torch.empty(256, device=DEV)
+    nb = a.zs_norm_workspace_bytes(300, 256)
+    a.zs_norm_backward(300, 256, dy, x, rstd, dx, dgamma=dg, kind="rms", workspace=garbage(nb), ws_bytes=nb)
+    zero, one = torch.zeros(256, dtype=torch.float64), torch.ones(256, dtype=torch.float64)
+    want = ref.norm_grad(keep[:, :256].cpu().double(), keep[:, 256:].cpu().double(), None, rstd.cpu().double(), one,
+                         torch.zeros(300, 256, dtype=torch.float64), "rms", torch.bfloat16, torch.float32, zero, zero)
+    within(dx, want["dx"], "dx")
+    within(dg, want["dgamma"], "dgamma")
+    assert torch.equal(b[:, :512], keep)
 
 
 def test_norm_grad_of_no_rows():
@@ -490,6 +507,27 @@ def test_embed_grad(dt, gdt):
         run_embed_grad(tokens, rows, cols, kind, dt, gdt, accumulate=i % 2 == 0, scale=cols ** 0.5, seed=i)
         run_embed_grad(tokens, rows, cols, kind, dt, gdt, accumulate=i % 2 == 1, scale=-0.3, seed=i, shift=1 + i,
                        gap=i + 1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_embed_grad_of_small_tables(kind):
+    """No more rows than buckets of the sort, with few and with many tokens each."""
+    for i, (tokens, rows) in enumerate([(300, 1), (3000, 1), (3000, 5), (16_384, 64), (16_384, 65), (900, 64)]):
+        run_embed_grad(tokens, rows, 16, kind, whole_numbers=True, seed=i, accumulate=i % 2 == 0)
+
+
+@pytest.mark.parametrize("kind", ["zipf", "one", "part"])
+def test_embed_grad_of_a_large_table(kind):
+    """Cleared by small workgroups beside the sort.  Whole numbers: any order gives the same sums."""
+    rows, cols, tokens = 140_001, 1000, 16_000
+    row = token_ids(tokens, rows, kind, 5).to(DEV)
+    dy = torch.randint(-4, 5, (tokens, cols), generator=gen(6)).bfloat16().to(DEV)
+    G = torch.full((rows, cols), 7.0, dtype=torch.bfloat16, device=DEV)
+    nb = a.zs_embed_workspace_bytes(tokens, rows, cols)
+    a.zs_embed_backward(tokens, row, rows, cols, dy, G, garbage(nb), nb)
+    inside = (row >= 0) & (row < rows)
+    want = torch.zeros(rows, cols, device=DEV).index_add_(0, row[inside], dy[inside].float())
+    assert torch.equal(G, want.bfloat16())
 
 
 def test_embed_grad_of_many_rows():

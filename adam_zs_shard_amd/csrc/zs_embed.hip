@@ -606,7 +606,7 @@ __device__ __forceinline__ int begin_of(uint64_t on, int l) {
   return begins ? 63 - __builtin_clzll(begins) : 0;
 }
 
-template <int W, int DT, int GDT, bool ADD>
+template <int W, int DT, int GDT, bool ADD, bool STREAM>
 __device__ __forceinline__ void sum_unit(const SumArgs& a, int64_t unit) {
   constexpr int V = kPack<DT>;
   const int lane = threadIdx.x % kWave;
@@ -649,9 +649,9 @@ __device__ __forceinline__ void sum_unit(const SumArgs& a, int64_t unit) {
     for (int u = 0; u < kLoads; ++u) {
       if (l + u >= end) break;
       const uint32_t t = __builtin_amdgcn_readlane(x.token, l + u);
-      p[u] = ld_some<DT>(reinterpret_cast<const char*>(a.dy.at + t * a.dy.pitch) +
-                             static_cast<int64_t>(c) * kSize<DT>,
-                         n);
+      p[u] = ld_some<DT, false, STREAM>(reinterpret_cast<const char*>(a.dy.at + t * a.dy.pitch) +
+                                            static_cast<int64_t>(c) * kSize<DT>,
+                                        n);
       if (ADD && !(x.on >> (l + u + 1) & 1))
         old[u] = ld_grad<V, GDT, ADD>(a, __builtin_amdgcn_readlane(x.row, l + u), c, n);
     }
@@ -678,10 +678,10 @@ __device__ __forceinline__ void sum_unit(const SumArgs& a, int64_t unit) {
   }
 }
 
-template <int W, int DT, int GDT, bool ADD>
+template <int W, int DT, int GDT, bool ADD, bool STREAM>
 __global__ __launch_bounds__(kBlock) void sum_kernel(SumArgs a) {
   for_units(static_cast<int64_t>(a.windows) * a.slabs,
-            [&](int64_t unit) { sum_unit<W, DT, GDT, ADD>(a, unit); });
+            [&](int64_t unit) { sum_unit<W, DT, GDT, ADD, STREAM>(a, unit); });
 }
 
 // A long row's sum: a workgroup per row and 256 columns, whose waves take equal
@@ -824,6 +824,14 @@ namespace {
 // 27 us, with 512 lanes 33).
 constexpr int64_t kClearLong = int64_t{256} << 20;
 
+// Up to so many bytes, dy may still be in the 256 MB cache where its rows are added to
+// a gradient, and is read through it (us through it and past it: 16384 x 1024 37.3 /
+// 39.9, 4096 x 4096 28.1 / 31.0, 32768 x 768 42.3 / 43.8, 131072 x 1024 122 / 106);
+// where the gradient was cleared before, that has filled the cache (16384 x 1024 52.0 /
+// 43.3, 32768 x 768 53.2 / 49.1).
+constexpr int64_t kSumCached = int64_t{64} << 20;
+static_assert(kWindowElems * 4 <= kSumCached, "few tokens' rows are read through it");
+
 hipError_t launch_sort(const EmbedGradLaunch& L, const EmbedLayout& lay) {
   SortArgs a;
   a.ids = L.ids;
@@ -917,7 +925,14 @@ hipError_t launch_embed_grad(const EmbedGradLaunch& L) {
         a.slabs = (L.cols + kSlab - 1) / kSlab;
         const int64_t groups = (static_cast<int64_t>(a.windows) * a.slabs + kWaves - 1) / kWaves;
         const dim3 grid(static_cast<unsigned>(groups < kMaxGroups ? groups : kMaxGroups));
-        sum_kernel<W, DT, GDT, ADD><<<grid, kBlock, 0, L.stream>>>(a);
+        if constexpr (ADD) {
+          if (W == kWindowFew || L.tokens * L.cols * kSize<DT> <= kSumCached) {
+            sum_kernel<W, DT, GDT, ADD, false><<<grid, kBlock, 0, L.stream>>>(a);
+            return;
+          }
+        }
+        if constexpr (!ADD || W == kWindowMany)
+          sum_kernel<W, DT, GDT, ADD, true><<<grid, kBlock, 0, L.stream>>>(a);
       });
       if (L.tokens <= W) return;  // no long row
       a.slabs = (L.cols + kJoinSlab - 1) / kJoinSlab;

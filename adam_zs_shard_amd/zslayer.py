@@ -168,7 +168,7 @@ def zs_norm_forward(rows: int, cols: int, x, y, gamma=None, beta=None, *, kind="
     st = call(pack(rows, cols, _named(kind, KINDS), dt, wdt, 0, eps, px, pr, pt, py, sx, sr, st_, sy,
                    _flat(gamma, tw), _flat(beta, tw), _flat(mean, f32), _flat(rstd, f32),
                    z._stream(stream) or 0))
-    if check:
+    if st and check:
         z._check(st, "zs_norm_forward")
     return st
 
@@ -197,7 +197,7 @@ def zs_norm_backward(rows: int, cols: int, dy, x, rstd, dx, *, mean=None, gamma=
                    sr, so, _flat(gamma, _torch.get(wdt)), _flat(mean, f32), _flat(rstd, f32),
                    _flat(dgamma, tg), _flat(dbeta, tg), z._addr(workspace) or 0, ws_bytes,
                    z._stream(stream) or 0))
-    if check:
+    if st and check:
         z._check(st, "zs_norm_backward")
     return st
 
@@ -215,7 +215,7 @@ def zs_embed_forward(tokens: int, ids, rows: int, cols: int, table, y, *, scale=
     st = call(pack(tokens, rows, cols, first_row, idt, dt, tdt, 0, scale, _flat(ids, ti),
                    _flat(table, tt), py, sy, _flat(pos_ids, ti), _flat(pos_table, tt), pos_rows,
                    z._stream(stream) or 0))
-    if check:
+    if st and check:
         z._check(st, "zs_embed_forward")
     return st
 
@@ -235,6 +235,6 @@ def zs_embed_backward(tokens: int, ids, rows: int, cols: int, dy, grad, workspac
     st = call(pack(tokens, rows, cols, first_row, idt, dt, gdt, int(accumulate), scale,
                    _flat(ids, _torch.get(idt)), pd, sd, _flat(grad, _torch.get(gdt)),
                    z._addr(workspace) or 0, ws_bytes, z._stream(stream) or 0))
-    if check:
+    if st and check:
         z._check(st, "zs_embed_backward")
     return st

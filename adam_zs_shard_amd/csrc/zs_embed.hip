@@ -57,7 +57,8 @@ __device__ __forceinline__ int64_t row_of(int64_t id, int64_t first, int64_t row
 
 // A lane takes one pack and ends: 8192 tokens of 768 bf16 with positions 5.7 us, 5.9
 // with two packs in flight, 7.4 with four; 16384 of 4096 34 us with one or two.
-template <int DT, int TDT, bool WIDE, bool POS>
+// WHOLE: rows of whole packs (the first 6.2 us without it).
+template <int DT, int TDT, bool WIDE, bool POS, bool WHOLE>
 __global__ __launch_bounds__(kBlock) void embed_kernel(EmbedArgs a) {
   constexpr int V = kPack<DT>;
   const int64_t all = a.tokens * a.packs;
@@ -72,21 +73,18 @@ __global__ __launch_bounds__(kBlock) void embed_kernel(EmbedArgs a) {
     if (t >= a.tokens) continue;
     const int64_t r = row_of(ld_id<WIDE>(a.ids, t), a.first_row, a.rows);
     const int64_t p = POS ? row_of(ld_id<WIDE>(a.pos_ids, t), 0, a.pos_rows) : -1;
-    Vals<V> f, g;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      f.v[i] = 0.0f;
-      g.v[i] = -0.0f;  // adds nothing
-    }
-    if (r >= 0) f = ld_vals<V, TDT>(a.table + (r * a.cols + c) * kSize<TDT>, n, 0.0f);
-    if (p >= 0) g = ld_vals<V, TDT>(a.pos_table + (p * a.cols + c) * kSize<TDT>, n, 0.0f);
+    Held<V, TDT> f{}, g{};
+    if (r >= 0) f = ld_held<V, TDT, WHOLE>(a.table + r * a.cols * kSize<TDT>, c, a.cols);
+    if (p >= 0) g = ld_held<V, TDT, WHOLE>(a.pos_table + p * a.cols * kSize<TDT>, c, a.cols);
+    settle_held<V, TDT, WHOLE>(f, c, a.cols);
+    if constexpr (POS) settle_held<V, TDT, WHOLE>(g, c, a.cols);
     float y[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      y[i] = r >= 0 ? f.v[i] * a.scale : 0.0f;  // +0, whatever the scale
-      if constexpr (POS) y[i] = y[i] + g.v[i];
+      y[i] = r >= 0 ? held(f, i) * a.scale : 0.0f;  // +0, whatever the scale
+      if constexpr (POS) y[i] = y[i] + (p >= 0 ? held(g, i) : -0.0f);  // -0 adds nothing
     }
-    st_some<DT>(reinterpret_cast<char*>(a.y.at + t * a.y.pitch) + c * kSize<DT>, n, narrow<DT>(y));
+    st_some<DT, WHOLE>(reinterpret_cast<char*>(a.y.at + t * a.y.pitch) + c * kSize<DT>, n, narrow<DT>(y));
   }
 }
 
@@ -477,75 +475,35 @@ struct SumArgs {
   float scale;
 };
 
-// V columns of a row of the gradient as they are held, so that several rows' take
-// few registers while they are in flight.
-template <int V, int GDT>
-struct Held {
-  uint32_t x[V * kSize<GDT> / 4];
-};
-template <int V, int GDT>
-__device__ __forceinline__ Held<V, GDT> ld_held(const char* at, int n) {
-  Held<V, GDT> h{};
-  constexpr int N = V * kSize<GDT> / 4;
-  if (n >= V) {
-    if constexpr (N == 2) {
-      const u32x2 q = *reinterpret_cast<const u32x2*>(at);
-      h.x[0] = q[0];
-      h.x[1] = q[1];
-    } else {
-#pragma unroll
-      for (int k = 0; k < N / 4; ++k) {
-        const u32x4 q = reinterpret_cast<const u32x4*>(at)[k];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h.x[4 * k + i] = q[i];
-      }
-    }
-  } else if (n > 0) {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i < n) {
-        if constexpr (GDT == kF32)
-          h.x[i] = reinterpret_cast<const uint32_t*>(at)[i];
-        else
-          h.x[i / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[i]) << (16 * (i % 2));
-      }
-  }
-  return h;
-}
-template <int V, int GDT>
-__device__ __forceinline__ float held(const Held<V, GDT>& h, int i) {
-  if constexpr (GDT == kF32) return __builtin_bit_cast(float, h.x[i]);
-  else return i % 2 == 0 ? widen_lo<GDT>(h.x[i / 2]) : widen_hi<GDT>(h.x[i / 2]);
-}
-
 // V columns of a row of the gradient, n of them there; old: what it holds.
-template <int V, int GDT, bool ADD>
+template <int V, int GDT, bool ADD, bool WHOLE>
 __device__ __forceinline__ void st_grad(const SumArgs& a, int64_t row, int c, int n, const Vals<V>& sum,
-                                        const Held<V, GDT>& old) {
+                                        Held<V, GDT> old) {
   Vals<V> f;
+  if constexpr (ADD) settle_held<V, GDT, WHOLE>(old, c, a.cols);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     f.v[i] = sum.v[i] * a.scale;
-    if constexpr (ADD) f.v[i] = held<V, GDT>(old, i) + f.v[i];
+    if constexpr (ADD) f.v[i] = held(old, i) + f.v[i];
   }
-  st_vals<V, GDT>(static_cast<char*>(a.grad) + (row * a.cols + c) * kSize<GDT>, n, f);
+  st_vals<V, GDT, WHOLE>(static_cast<char*>(a.grad) + (row * a.cols + c) * kSize<GDT>, n, f);
 }
-template <int V, int GDT, bool ADD>
-__device__ __forceinline__ Held<V, GDT> ld_grad(const SumArgs& a, int64_t row, int c, int n) {
+template <int V, int GDT, bool ADD, bool WHOLE>
+__device__ __forceinline__ Held<V, GDT> ld_grad(const SumArgs& a, int64_t row, int c) {
   if constexpr (ADD)
-    return ld_held<V, GDT>(static_cast<const char*>(a.grad) + (row * a.cols + c) * kSize<GDT>, n);
+    return ld_held<V, GDT, WHOLE>(static_cast<const char*>(a.grad) + row * a.cols * kSize<GDT>, c, a.cols);
   return Held<V, GDT>{};
 }
 
 // V sums, n of them there, through the cache: the next kernel reads them.
-template <int V>
+template <int V, bool WHOLE>
 __device__ __forceinline__ void st_sums(float* to, int n, const Vals<V>& x) {
 #pragma unroll
   for (int k = 0; k < V / 4; ++k) {
     if (n >= 4 * k + 4) {
       *reinterpret_cast<f32x4*>(to + 4 * k) =
           f32x4{x.v[4 * k], x.v[4 * k + 1], x.v[4 * k + 2], x.v[4 * k + 3]};
-    } else {
+    } else if (!WHOLE) {
 #pragma unroll
       for (int i = 4 * k; i < 4 * k + 4; ++i)
         if (i < n) to[i] = x.v[i];
@@ -608,7 +566,7 @@ __device__ __forceinline__ int begin_of(uint64_t on, int l) {
   return begins ? 63 - __builtin_clzll(begins) : 0;
 }
 
-template <int W, int DT, int GDT, bool ADD, bool STREAM>
+template <int W, int DT, int GDT, bool ADD, bool STREAM, bool WHOLE>
 __device__ __forceinline__ void sum_unit(const SumArgs& a, int64_t unit) {
   constexpr int V = kPack<DT>;
   const int lane = threadIdx.x % kWave;
@@ -651,16 +609,16 @@ __device__ __forceinline__ void sum_unit(const SumArgs& a, int64_t unit) {
     for (int u = 0; u < kLoads; ++u) {
       if (l + u >= end) break;
       const uint32_t t = __builtin_amdgcn_readlane(x.token, l + u);
-      p[u] = ld_some<DT, false, STREAM>(reinterpret_cast<const char*>(a.dy.at + t * a.dy.pitch) +
-                                            static_cast<int64_t>(c) * kSize<DT>,
-                                        n);
+      p[u] = ld_some<DT, WHOLE, STREAM>(reinterpret_cast<const char*>(a.dy.at + t * a.dy.pitch), c,
+                                        a.cols);
       if (ADD && !(x.on >> (l + u + 1) & 1))
-        old[u] = ld_grad<V, GDT, ADD>(a, __builtin_amdgcn_readlane(x.row, l + u), c, n);
+        old[u] = ld_grad<V, GDT, ADD, WHOLE>(a, __builtin_amdgcn_readlane(x.row, l + u), c);
     }
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       if (l + u >= end) break;
       float f[V];
+      settle<DT, WHOLE>(p[u], c, a.cols);
       widen<DT>(p[u], f);
 #pragma unroll
       for (int i = 0; i < V; ++i) sum.v[i] = sum.v[i] + f[i];
@@ -669,9 +627,9 @@ __device__ __forceinline__ void sum_unit(const SumArgs& a, int64_t unit) {
       const bool part = head || (last && tail);
       if (part) {
         float* to = a.partial + (2 * w + (head ? 0 : 1)) * a.cols + c;
-        st_sums<V>(to, n, sum);
+        st_sums<V, WHOLE>(to, n, sum);
       } else {
-        st_grad<V, GDT, ADD>(a, __builtin_amdgcn_readlane(x.row, l + u), c, n, sum, old[u]);
+        st_grad<V, GDT, ADD, WHOLE>(a, __builtin_amdgcn_readlane(x.row, l + u), c, n, sum, old[u]);
       }
       head = false;
 #pragma unroll
@@ -680,10 +638,10 @@ __device__ __forceinline__ void sum_unit(const SumArgs& a, int64_t unit) {
   }
 }
 
-template <int W, int DT, int GDT, bool ADD, bool STREAM>
+template <int W, int DT, int GDT, bool ADD, bool STREAM, bool WHOLE>
 __global__ __launch_bounds__(kBlock) void sum_kernel(SumArgs a) {
   for_units(static_cast<int64_t>(a.windows) * a.slabs,
-            [&](int64_t unit) { sum_unit<W, DT, GDT, ADD, STREAM>(a, unit); });
+            [&](int64_t unit) { sum_unit<W, DT, GDT, ADD, STREAM, WHOLE>(a, unit); });
 }
 
 // A long row's sum: a workgroup per row and 256 columns, whose waves take equal
@@ -694,7 +652,7 @@ __global__ __launch_bounds__(kBlock) void sum_kernel(SumArgs a) {
 // 8192 tokens.
 constexpr int kJoinV = 4, kJoinSlab = kWave * kJoinV, kJoinLoads = 8, kJoinWaves = 8;
 
-template <int W, int GDT, bool ADD>
+template <int W, int GDT, bool ADD, bool WHOLE>
 __global__ __launch_bounds__(kJoinWaves * kWave) void sum_join_kernel(SumArgs a) {
   __shared__ Vals<kJoinV> sums[kJoinWaves][kWave];
   const int lane = threadIdx.x % kWave;
@@ -705,7 +663,7 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void sum_join_kernel(SumArgs a)
     const int c = (static_cast<int>(unit - k * a.slabs) * kWave + lane) * kJoinV, n = a.cols - c;
     const uint32_t row = a.list[(w + 1) * W].row;
     Held<kJoinV, GDT> old{};
-    if (wave == 0) old = ld_grad<kJoinV, GDT, ADD>(a, row, c, n);
+    if (wave == 0) old = ld_grad<kJoinV, GDT, ADD, WHOLE>(a, row, c);
     int64_t more = 1;  // windows after w that it meets
     // of the next 64, or of each 64th, those up to the first that it does not meet
     const auto meets = [&](int64_t step) -> int64_t {
@@ -727,19 +685,21 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void sum_join_kernel(SumArgs a)
 #pragma unroll
     for (int i = 0; i < kJoinV; ++i) sum.v[i] = 0.0f;
     for (int64_t i = wave * each; i < i1; i += kJoinLoads) {
-      Vals<kJoinV> f[kJoinLoads];
+      Held<kJoinV, kF32> f[kJoinLoads];
 #pragma unroll
       for (int u = 0; u < kJoinLoads; ++u) {
-#pragma unroll
-        for (int q = 0; q < kJoinV; ++q) f[u].v[q] = 0.0f;
         const int64_t at = i + u == 0 ? 2 * w + 1 : 2 * (w + i + u);
-        if (i + u < i1 && n > 0)
-          f[u] = ld_vals<kJoinV, kF32>(reinterpret_cast<const char*>(a.partial + at * a.cols + c), n, 0.0f);
+        f[u] = Held<kJoinV, kF32>{};
+        if (i + u < i1)
+          f[u] = ld_held<kJoinV, kF32, WHOLE>(reinterpret_cast<const char*>(a.partial + at * a.cols), c,
+                                              a.cols);
       }
 #pragma unroll
-      for (int u = 0; u < kJoinLoads; ++u)
+      for (int u = 0; u < kJoinLoads; ++u) {
+        settle_held<kJoinV, kF32, WHOLE>(f[u], c, a.cols);
 #pragma unroll
-        for (int q = 0; q < kJoinV; ++q) sum.v[q] = sum.v[q] + f[u].v[q];
+        for (int q = 0; q < kJoinV; ++q) sum.v[q] = sum.v[q] + held(f[u], q);
+      }
     }
     sums[wave][lane] = sum;
     __syncthreads();
@@ -748,7 +708,7 @@ __global__ __launch_bounds__(kJoinWaves * kWave) void sum_join_kernel(SumArgs a)
       for (int i = 1; i < kJoinWaves; ++i)
 #pragma unroll
         for (int q = 0; q < kJoinV; ++q) sum.v[q] = sum.v[q] + sums[i][lane].v[q];
-      st_grad<kJoinV, GDT, ADD>(a, row, c, n, sum, old);
+      st_grad<kJoinV, GDT, ADD, WHOLE>(a, row, c, n, sum, old);
     }
     __syncthreads();
   }
@@ -809,8 +769,9 @@ hipError_t launch_embed(const EmbedLaunch& L) {
     with_gdt(L.tdt, [&](auto t) {
       constexpr int TDT = decltype(t)::value;
       const auto go = [&](auto wide, auto pos) {
-        embed_kernel<DT, TDT, decltype(wide)::value != 0, decltype(pos)::value != 0>
-            <<<grid, kBlock, 0, L.stream>>>(a);
+        constexpr bool WIDE = decltype(wide)::value != 0, POS = decltype(pos)::value != 0;
+        if (a.cols % kPack<DT> == 0) embed_kernel<DT, TDT, WIDE, POS, true><<<grid, kBlock, 0, L.stream>>>(a);
+        else embed_kernel<DT, TDT, WIDE, POS, false><<<grid, kBlock, 0, L.stream>>>(a);
       };
       const auto pick = [&](auto wide) { L.pos_table ? go(wide, IC<1>{}) : go(wide, IC<0>{}); };
       L.wide_ids ? pick(IC<1>{}) : pick(IC<0>{});
@@ -927,21 +888,28 @@ hipError_t launch_embed_grad(const EmbedGradLaunch& L) {
         a.slabs = (L.cols + kSlab - 1) / kSlab;
         const int64_t groups = (static_cast<int64_t>(a.windows) * a.slabs + kWaves - 1) / kWaves;
         const dim3 grid(static_cast<unsigned>(groups < kMaxGroups ? groups : kMaxGroups));
-        if constexpr (ADD) {
-          if (W == kWindowFew || L.tokens * L.cols * kSize<DT> <= kSumCached) {
-            sum_kernel<W, DT, GDT, ADD, false><<<grid, kBlock, 0, L.stream>>>(a);
-            return;
+        const auto sum = [&](auto whole) {
+          constexpr bool WHOLE = decltype(whole)::value != 0;
+          if constexpr (ADD) {
+            if (W == kWindowFew || L.tokens * L.cols * kSize<DT> <= kSumCached) {
+              sum_kernel<W, DT, GDT, ADD, false, WHOLE><<<grid, kBlock, 0, L.stream>>>(a);
+              return;
+            }
           }
-        }
-        if constexpr (!ADD || W == kWindowMany)
-          sum_kernel<W, DT, GDT, ADD, true><<<grid, kBlock, 0, L.stream>>>(a);
+          if constexpr (!ADD || W == kWindowMany)
+            sum_kernel<W, DT, GDT, ADD, true, WHOLE><<<grid, kBlock, 0, L.stream>>>(a);
+        };
+        L.cols % kPack<DT> == 0 ? sum(IC<1>{}) : sum(IC<0>{});
       });
       if (L.tokens <= W) return;  // no long row
       a.slabs = (L.cols + kJoinSlab - 1) / kJoinSlab;
       const int64_t most = int64_t{cu_count()} * (32 / kJoinWaves);
       const int64_t units = L.tokens / (W + 1) * a.slabs;
       const dim3 grid(static_cast<unsigned>(units < most ? units : most));
-      sum_join_kernel<W, GDT, ADD><<<grid, kJoinWaves * kWave, 0, L.stream>>>(a);
+      if (L.cols % kJoinV == 0)
+        sum_join_kernel<W, GDT, ADD, true><<<grid, kJoinWaves * kWave, 0, L.stream>>>(a);
+      else
+        sum_join_kernel<W, GDT, ADD, false><<<grid, kJoinWaves * kWave, 0, L.stream>>>(a);
     };
     const auto pick = [&](auto w) { L.accumulate ? go(IC<1>{}, w) : go(IC<0>{}, w); };
     window == kWindowFew ? pick(IC<kWindowFew>{}) : pick(IC<kWindowMany>{});

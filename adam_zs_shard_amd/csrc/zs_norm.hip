@@ -36,7 +36,7 @@ __device__ __forceinline__ void ld_row(const Rows& rows, int64_t r, int lane, in
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c = (lane + j * TEAM) * kPack<DT>;
-    q[j] = ld_some<DT, WHOLE, STREAM>(at + c * kSize<DT>, cols - c);
+    q[j] = ld_some<DT, WHOLE, STREAM>(at, c, cols);
   }
 }
 
@@ -51,8 +51,8 @@ __global__ __launch_bounds__(WG) void norm_kernel(NormArgs a) {
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c = (lane + j * TEAM) * V;
-    gamma[j] = ld_weights<V>(a.gamma, a.wdt, c, a.cols - c, 1.0f);
-    beta[j] = ld_weights<V>(a.beta, a.wdt, c, a.cols - c, 0.0f);
+    gamma[j] = ld_weights<V>(a.gamma, a.wdt, c, a.cols, 1.0f);
+    beta[j] = ld_weights<V>(a.beta, a.wdt, c, a.cols, 0.0f);
   }
   const float n = static_cast<float>(a.cols);
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * TEAMS; r0 < a.rows;
@@ -62,14 +62,17 @@ __global__ __launch_bounds__(WG) void norm_kernel(NormArgs a) {
     float t[J][V];
     Pack<DT> q[J];
     ld_row<DT, TEAM, J, WHOLE, STREAM>(a.x, r, lane, a.cols, q);
+    Pack<DT> p[J];
+    if (a.residual.at) ld_row<DT, TEAM, J, WHOLE, STREAM>(a.residual, r, lane, a.cols, p);
+#pragma unroll
+    for (int j = 0; j < J; ++j) settle<DT, WHOLE>(q[j], (lane + j * TEAM) * V, a.cols);
     if (a.residual.at) {
       char* total = reinterpret_cast<char*>(a.total.at + r * a.total.pitch);
-      Pack<DT> p[J];
-      ld_row<DT, TEAM, J, WHOLE, STREAM>(a.residual, r, lane, a.cols, p);
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int c = (lane + j * TEAM) * V;
         float f[V];
+        settle<DT, WHOLE>(p[j], c, a.cols);
         widen<DT>(q[j], t[j]);
         widen<DT>(p[j], f);
 #pragma unroll

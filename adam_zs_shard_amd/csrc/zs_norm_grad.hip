@@ -45,8 +45,8 @@ __device__ __forceinline__ GradRow<DT, J> ld_grad_row(const NormGradArgs& a, int
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c = (lane + j * TEAM) * kPack<DT>;
-    g.dy[j] = ld_some<DT, WHOLE>(dy + c * kSize<DT>, a.cols - c);
-    g.x[j] = ld_some<DT, WHOLE>(x + c * kSize<DT>, a.cols - c);
+    g.dy[j] = ld_some<DT, WHOLE>(dy, c, a.cols);
+    g.x[j] = ld_some<DT, WHOLE>(x, c, a.cols);
   }
   if constexpr (LAYER) g.mean = a.mean[r];
   g.rstd = a.rstd[r];
@@ -97,17 +97,19 @@ __device__ __forceinline__ void column_sums(const NormGradArgs& a, int slab) {
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       const int64_t q = r + u * kRows;
-      const int there = q < a.rows ? n : 0;
+      const int there = q < a.rows ? a.cols : 0;  // columns of the row
       const char* at_dy = reinterpret_cast<const char*>(a.dy.at + q * a.dy.pitch);
       const char* at_x = reinterpret_cast<const char*>(a.x.at + q * a.x.pitch);
-      dy[u] = ld_some<DT, WHOLE, false>(at_dy + c * kSize<DT>, there);
-      x[u] = ld_some<DT, WHOLE, false>(at_x + c * kSize<DT>, there);
+      dy[u] = ld_some<DT, WHOLE, false>(at_dy, c, there);
+      x[u] = ld_some<DT, WHOLE, false>(at_x, c, there);
       mean[u] = LAYER && there > 0 ? a.mean[q] : 0.0f;
       rstd[u] = there > 0 ? a.rstd[q] : 0.0f;
     }
 #pragma unroll
     for (int u = 0; u < kLoads; ++u) {
       float h[V], t[V];
+      settle<DT, WHOLE>(dy[u], c, a.cols);
+      settle<DT, WHOLE>(x[u], c, a.cols);
       normed<DT, LAYER, WHOLE>(x[u], mean[u], rstd[u], r + u * kRows < a.rows ? n : 0, h);
       widen<DT>(dy[u], t);
 #pragma unroll
@@ -162,7 +164,7 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
   for (int j = 0; j < J; ++j) {
     const int c = (lane + j * TEAM) * V;
-    gamma[j] = ld_weights<V>(a.gamma, a.wdt, c, a.cols - c, 1.0f);
+    gamma[j] = ld_weights<V>(a.gamma, a.wdt, c, a.cols, 1.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) acc_g[j][i] = acc_b[j][i] = 0.0f;
   }
@@ -178,14 +180,17 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const int c = (lane + j * TEAM) * V;
-        dres[j] = ld_some<DT, WHOLE>(at + c * kSize<DT>, a.cols - c);
+        dres[j] = ld_some<DT, WHOLE>(at, c, a.cols);
       }
     }
     float s[LAYER ? 2 : 1] = {};
 #pragma unroll
     for (int j = 0; j < J; ++j) {
+      const int c = (lane + j * TEAM) * V;
       float h[V], t[V];
-      normed<DT, LAYER, WHOLE>(g.x[j], g.mean, g.rstd, a.cols - (lane + j * TEAM) * V, h);
+      settle<DT, WHOLE>(g.dy[j], c, a.cols);
+      settle<DT, WHOLE>(g.x[j], c, a.cols);
+      normed<DT, LAYER, WHOLE>(g.x[j], g.mean, g.rstd, a.cols - c, h);
       widen<DT>(g.dy[j], t);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -219,6 +224,7 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
         t[i] = (t[i] - h[i] * c2) * g.rstd;
       }
       if (a.dres.at) {
+        settle<DT, WHOLE>(dres[j], c, a.cols);
         widen<DT>(dres[j], h);
 #pragma unroll
         for (int i = 0; i < V; ++i) t[i] = t[i] + h[i];

@@ -163,6 +163,16 @@ def test_norm_in_place(place, cols):
         run_norm(50, cols, "rms", "f16", place=place)
 
 
+REMAINDERS = [*range(1, 25), *range(1040, 1048)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cols", REMAINDERS)
+def test_norm_of_every_remainder(cols, dt):
+    run_norm(9, cols, "layer", dt, "f16", residual=True, shift=1, gap=1, seed=cols)
+    run_norm(9, cols, "rms", dt, "f32", residual=True, gap=2, place="total=x", seed=cols)
+
+
 def test_norm_of_columns_of_one_buffer():
     """Input and output side by side in the same rows."""
     b = torch.randn(9, 3 * 700, generator=gen(3)).bfloat16().to(DEV)
@@ -294,6 +304,14 @@ def test_norm_grad_in_place(place, rows, cols):
     run_norm_grad(rows, cols, "layer", "bf16", dres=True, place=place)
 
 
+@pytest.mark.parametrize("dt,gdt", [("bf16", "f16"), ("f16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("cols", REMAINDERS)
+def test_norm_grad_of_every_remainder(cols, dt, gdt):
+    for rows in (9, 1100):
+        run_norm_grad(rows, cols, "layer", dt, "f16", gdt, dres=True, accumulate=True, shift=1, gap=1, seed=cols)
+        run_norm_grad(rows, cols, "rms", dt, "f32", gdt, gap=2, place="dx=dy", seed=cols)
+
+
 def test_norm_grad_of_columns_of_one_buffer():
     """dy, x and dx side by side in the same rows, few enough to be read twice."""
     g = gen(4)
@@ -413,6 +431,12 @@ def test_embed(dt, tdt):
         run_embed(tokens, rows, cols, dt, tdt, seed=i, shift=1 + i, gap=i, pos=((i + 1) % 3) * 5, first=7)
 
 
+@pytest.mark.parametrize("dt,tdt", [("bf16", "f16"), ("f16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("cols", REMAINDERS)
+def test_embed_of_every_remainder(cols, dt, tdt):
+    run_embed(40, 30, cols, dt, tdt, seed=cols, pos=20, shift=1, gap=1, scale=3.3)
+
+
 def test_embed_ids_of_any_value():
     extremes = torch.tensor([0, 1, 49, 50, -1, 2**31 - 1, -2**31, 2**31, 2**32, 2**32 + 3, 2**63 - 1, -2**63, 7])
     run_embed(13, 50, 100, "f32", "f32", ids=extremes)
@@ -507,6 +531,15 @@ def test_embed_grad(dt, gdt):
         run_embed_grad(tokens, rows, cols, kind, dt, gdt, accumulate=i % 2 == 0, scale=cols ** 0.5, seed=i)
         run_embed_grad(tokens, rows, cols, kind, dt, gdt, accumulate=i % 2 == 1, scale=-0.3, seed=i, shift=1 + i,
                        gap=i + 1)
+
+
+@pytest.mark.parametrize("dt,gdt", [("bf16", "f16"), ("f16", "f32"), ("f32", "bf16")])
+@pytest.mark.parametrize("cols", REMAINDERS)
+def test_embed_grad_of_every_remainder(cols, dt, gdt):
+    """Short rows, long ones, and rows that the gradient already holds."""
+    for kind in ("each", "zipf"):
+        run_embed_grad(300, 20, cols, kind, dt, gdt, accumulate=kind == "zipf", seed=cols, shift=1, gap=1)
+        run_embed_grad(300, 20, cols, kind, dt, gdt, accumulate=kind == "each", seed=cols)
 
 
 @pytest.mark.parametrize("kind", KINDS)

@@ -30,7 +30,7 @@ hipError_t launch_norm(const NormLaunch& L);
 // Workgroups of the norm's backward pass at most, each with one row of partial
 // sums per gradient in the workspace.
 constexpr int kNormParts = 512;
-// Columns of such a row: what the lanes of a team hold, 8 or 16 columns each.
+// Columns of such a row at most: what the lanes of a team hold, 8 or 16 columns each.
 constexpr int norm_width(int cols) {
   int width = 512;
   while (width < cols) width *= 2;

@@ -220,14 +220,18 @@ __device__ __forceinline__ float dpp_add(float x) {
                  float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf,
                                                     true));
 }
-// The sum of the wave's values, in a fixed order, in every lane.  Every lane
-// must be active.
-__device__ __forceinline__ float wave_sum(float x) {
+// The sum of the values of the lane's 16, 32 or 64, in a fixed order, in every lane.
+// Every one of these must be active.
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float x) {
   x = dpp_add<0xb1>(x);   // lanes xor 1
   x = dpp_add<0x4e>(x);   // xor 2
   x = dpp_add<0x141>(x);  // mirrored in eights
   x = dpp_add<0x140>(x);  // mirrored in sixteens
   const int b = __builtin_bit_cast(int, x);
+  if constexpr (LANES == 16) return x;
+  if constexpr (LANES == 32)
+    return x + __builtin_bit_cast(float, __builtin_amdgcn_ds_swizzle(b, 0x401f));  // xor 16
   const float r0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 0));
   const float r1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 16));
   const float r2 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(b, 32));

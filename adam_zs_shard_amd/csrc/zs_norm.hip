@@ -7,7 +7,7 @@
 // 4096 bf16: forward with a residual 85.7 us, 6.3 TB/s; backward 88.5, 6.1, and 4.8
 // for the second launch), and latency where they are narrow (8192 x 768: 7.3 and 15
 // us) or few.  A row stays in the registers of a team of lanes from its only load to
-// its store, so a team has 64 to 1024 lanes by the row's length, and the sums over
+// its store, so a team has 16 to 1024 lanes by the row's length, and the sums over
 // it are sums over the team: DPP adds in a wave, LDS between waves.  The variance is
 // the sum of squares of what remains after the mean is taken off, not the difference
 // of two sums, which loses its digits where the mean is large.
@@ -46,7 +46,7 @@ __global__ __launch_bounds__(WG) void norm_kernel(NormArgs a) {
   __shared__ float part[2][1][16];
   int turn = 0;
   const int lane = threadIdx.x % TEAM;
-  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM);
+  const int team = team_of<TEAM>();
   Vals<V> gamma[J], beta[J];
 #pragma unroll
   for (int j = 0; j < J; ++j) {
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(WG) void norm_kernel(NormArgs a) {
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * TEAMS; r0 < a.rows;
        r0 += static_cast<int64_t>(gridDim.x) * TEAMS) {
     const int64_t r = r0 + team;
-    if (TEAMS > 1 && r >= a.rows) return;  // a team of one wave waits for nobody
+    if (TEAMS > 1 && r >= a.rows) return;  // such a team waits for nobody
     float t[J][V];
     Pack<DT> q[J];
     ld_row<DT, TEAM, J, WHOLE, STREAM>(a.x, r, lane, a.cols, q);
@@ -134,7 +134,7 @@ constexpr int kNormHeld = 16384;
 // there by the kernel before (32768 x 1024 bf16 22.4 us, read past it 27.4).
 constexpr int64_t kNormCached = int64_t{192} << 20;
 
-constexpr int norm_group(int team) { return team == kWave ? 4 * kWave : team; }
+constexpr int norm_group(int team) { return team <= kWave ? 4 * kWave : team; }
 
 }  // namespace
 

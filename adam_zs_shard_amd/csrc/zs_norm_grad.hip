@@ -158,7 +158,7 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
   extern __shared__ float sums[];  // WG * E, where there are several teams
   int turn = 0;
   const int lane = threadIdx.x % TEAM;
-  const int team = __builtin_amdgcn_readfirstlane(threadIdx.x / TEAM);
+  const int team = team_of<TEAM>();
   Vals<V> gamma[J];
   float acc_g[J][V], acc_b[J][V];
 #pragma unroll

@@ -163,6 +163,18 @@ def test_norm_in_place(place, cols):
         run_norm(50, cols, "rms", "f16", place=place)
 
 
+# teams of 16, 32 and 64 lanes, whole and broken waves and workgroups of them
+NARROW = [(1, 128), (3, 64), (5, 129), (17, 127), (31, 256), (33, 255), (63, 128), (1025, 192), (4097, 257),
+          (20_000, 128), (33_000, 65), (9000, 512)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols", NARROW)
+def test_norm_of_narrow_rows(rows, cols, dt):
+    run_norm(rows, cols, "layer", dt, "f32", residual=True, gap=cols, seed=rows)
+    run_norm(rows, cols, "rms", dt, seed=rows, place="y=x")
+
+
 REMAINDERS = [*range(1, 25), *range(1040, 1048)]
 
 
@@ -302,6 +314,13 @@ def test_norm_grad_of_what_is_wanted(kind, want):
 @pytest.mark.parametrize("rows,cols", [(2500, 100), (2500, 768), (2500, 6000), (400, 768), (90, 5000), (1, 31)])
 def test_norm_grad_in_place(place, rows, cols):
     run_norm_grad(rows, cols, "layer", "bf16", dres=True, place=place)
+
+
+@pytest.mark.parametrize("dt,gdt", [("bf16", "f32"), ("f16", "f16"), ("f32", "f32")])
+@pytest.mark.parametrize("rows,cols", NARROW)
+def test_norm_grad_of_narrow_rows(rows, cols, dt, gdt):
+    run_norm_grad(rows, cols, "layer", dt, "f32", gdt, dres=True, accumulate=True, gap=cols, seed=rows)
+    run_norm_grad(rows, cols, "rms", dt, gdt=gdt, seed=rows, place="dx=x")
 
 
 @pytest.mark.parametrize("dt,gdt", [("bf16", "f16"), ("f16", "f32"), ("f32", "bf16")])

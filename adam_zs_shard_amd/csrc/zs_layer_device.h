@@ -19,6 +19,8 @@ struct Pack {
   std::conditional_t<DT == kF32, f32x4, u32x4> x;
 };
 
+typedef uint32_t Word __attribute__((aligned(2)));
+
 template <int V>
 struct Vals {
   float v[V];
@@ -141,19 +143,34 @@ __device__ __forceinline__ Pack<DT> narrow(const float (&f)[kPack<DT>]) {
   return q;
 }
 
+// The first `halves` halves of N words, fewer than all: in up to three stores.
+template <int N, class T>
+__device__ __forceinline__ void st_part(char* at, int halves, T x) {
+  uint32_t w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = x[i];
+  if constexpr (N == 4) {
+    if (halves & 4) {
+      __builtin_nontemporal_store(u32x2{w[0], w[1]}, reinterpret_cast<u32x2*>(at));
+      w[0] = w[2];
+      w[1] = w[3];
+      at += 8;
+    }
+  }
+  if (halves & 2) {
+    *reinterpret_cast<Word*>(at) = w[0];
+    w[0] = w[1];
+    at += 4;
+  }
+  if (halves & 1) *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>(w[0]);
+}
 template <int DT, bool WHOLE = false>
 __device__ __forceinline__ void st_some(char* at, int n, const Pack<DT>& q) {
   if (n >= kPack<DT>) {
     __builtin_nontemporal_store(q.x, reinterpret_cast<decltype(Pack<DT>::x)*>(at));
   } else if (!WHOLE && n > 0) {
-#pragma unroll
-    for (int i = 0; i < kPack<DT>; ++i)
-      if (i < n) {
-        if constexpr (DT == kF32)
-          reinterpret_cast<float*>(at)[i] = q.x[i];
-        else
-          reinterpret_cast<uint16_t*>(at)[i] = static_cast<uint16_t>(q.x[i / 2] >> (16 * (i % 2)));
-      }
+    const auto x = __builtin_bit_cast(u32x4, q.x);
+    st_part<4>(at, n * (kSize<DT> / 2), x);
   }
 }
 
@@ -173,9 +190,7 @@ __device__ __forceinline__ void st_vals(char* at, int n, const Vals<V>& x) {
     if (n >= 4) {
       __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(at));
     } else if (!WHOLE) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < n) reinterpret_cast<uint16_t*>(at)[i] = static_cast<uint16_t>(q[i / 2] >> (16 * (i % 2)));
+      if (n > 0) st_part<2>(at, n, q);
     }
   }
 }

@@ -30,8 +30,8 @@ struct Vals {
 // A row's last elements, if they are fewer than V, come with a load of the row's last
 // V, and settle_held() puts them first and zeros behind them, after all loads of a
 // lane are on their way.  Element by element they were up to V - 1 loads that waited
-// for one another: norms' backward pass, 742 x 1043 fp16 16.3 us, now 9.6, 20,000 x
-// 1001 bf16 46.6 / 36.7; the table's gradient, 43,231 x 1017 bf16 65.6 / 55.5.
+// for one another: norms' backward pass, 742 x 1043 fp16 16.3 us, now 9.5, 20,000 x
+// 1001 bf16 46.6 / 35.8; the table's gradient, 43,231 x 1017 bf16 65.6 / 55.5.
 // STREAM: non-temporal.  WHOLE: cols is a multiple of V, and there is nothing to settle.
 template <int V, int DT>
 struct Held {

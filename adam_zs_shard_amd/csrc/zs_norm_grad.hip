@@ -64,9 +64,9 @@ __device__ __forceinline__ void forget(Pack<DT>& q) {
   }
 }
 
-// h = (x - mean) * rstd of a pack, zeros where the row has ended within it.  Packs
-// wholly beyond the row (WHOLE) give values that only products with their dy, which
-// is 0, see.
+// h = (x - mean) * rstd of a pack, zeros where the row has ended within it.  Of packs
+// wholly beyond the row (WHOLE) it is -mean * rstd, which may be infinite: a row's sums
+// leave it out.
 template <int DT, bool LAYER, bool WHOLE>
 __device__ __forceinline__ void normed(const Pack<DT>& x, float mean, float rstd, int left,
                                        float (&h)[kPack<DT>]) {
@@ -192,6 +192,7 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
       settle<DT, WHOLE>(g.x[j], c, a.cols);
       normed<DT, LAYER, WHOLE>(g.x[j], g.mean, g.rstd, a.cols - c, h);
       widen<DT>(g.dy[j], t);
+      const float before = s[0];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         acc_g[j][i] = __builtin_fmaf(t[i], h[i], acc_g[j][i]);
@@ -200,6 +201,8 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
         s[0] = __builtin_fmaf(t[i], h[i], s[0]);
         if constexpr (LAYER) s[1] += t[i];
       }
+      // beyond the row t is 0, but 0 * h need not be
+      if (WHOLE && c >= a.cols) s[0] = before;
     }
     team_sums<TEAM>(s, part, turn);
     const float c2 = s[0] / n, c1 = LAYER ? s[LAYER ? 1 : 0] / n : 0.0f;

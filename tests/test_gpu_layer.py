@@ -374,6 +374,40 @@ def test_norm_grad_of_non_finite_rows():
     assert torch.equal(out[0][1][cols], out[1][1][cols]) and not torch.isfinite(out[1][1][3])
 
 
+@pytest.mark.parametrize("dt,cols", [("bf16", c) for c in (8, 72, 136, 264, 520, 768, 1032, 2056, 4104, 5120, 8200, 9000)]
+                         + [("f32", c) for c in (4, 36, 132, 260, 516, 1028, 8196, 9000)] + [("f32", 9001), ("bf16", 71)])
+@pytest.mark.parametrize("rows", [3, 1100])
+def test_norm_grad_of_huge_equal_values(dt, cols, rows):
+    """mean * rstd is beyond fp32 and x - mean is 0: the lanes of a team behind a row's last element see
+    the mean, and not the row."""
+    x = Buf(rows, cols, TD[dt], values=torch.full((rows, cols), 2.0 ** 110)).t
+    dy = Buf(rows, cols, TD[dt], values=torch.randn(rows, cols, generator=gen(cols))).t
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    gamma = weights(cols, "bf16", 5, (True, False))[0]
+    a.zs_norm_forward(rows, cols, x, y, gamma, eps=1e-12, mean=mean, rstd=rstd)
+    dg, db = torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+    nb = a.zs_norm_workspace_bytes(rows, cols)
+    a.zs_norm_backward(rows, cols, dy, x, rstd, dx, mean=mean, gamma=gamma, dgamma=dg, dbeta=db,
+                       workspace=garbage(nb), ws_bytes=nb)
+    assert bool((mean == 2.0 ** 110).all()) and bool((rstd * 2.0 ** 110 == float("inf")).all())
+    zero = torch.zeros(rows, cols, dtype=torch.float64)
+    want = ref.norm_grad(dy.cpu().double(), x.cpu().double(), mean.cpu().double(), rstd.cpu().double(),
+                         wide(gamma, cols, 1.0), zero, "layer", TD[dt], torch.float32, zero[0], zero[0])
+    for got, name in ((dx, "dx"), (dg, "dgamma"), (db, "dbeta")):
+        within(got, want[name], name)
+
+
+@pytest.mark.parametrize("cols", [4, 35, 36, 128, 516, 768, 9000])
+def test_norm_grad_of_an_infinite_rstd(cols):
+    """Squares that vanish and no eps: h and c2 are +inf, so dx = (1 - inf * inf) * inf, whatever the width."""
+    x, one = torch.full((3, cols), 1e-30, device=DEV), torch.ones(3, cols, device=DEV)
+    y, dx, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(3, device=DEV)
+    a.zs_norm_forward(3, cols, x, y, kind="rms", eps=0.0, rstd=rstd)
+    a.zs_norm_backward(3, cols, one, x, rstd, dx, kind="rms")
+    assert bool((rstd == float("inf")).all()) and bool((dx == -float("inf")).all())
+
+
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_norm_grad_against_differences(kind):
     """Along a direction d: the outputs of two forward passes 2h apart, in fp32.  Each output is off

@@ -747,6 +747,19 @@ EmbedLayout embed_layout(int64_t tokens, int64_t cols) {
   return l;
 }
 
+// The layout grows with the tokens, but for steps down where windows get longer (few
+// tokens are the most before) and where tiles do (every multiple of kTiles tokens is).
+size_t embed_workspace(int64_t tokens, int64_t cols) {
+  constexpr int64_t kTiles = int64_t{kTilesMost} * kTileStep;
+  const int64_t few = kWindowElems / cols < tokens ? kWindowElems / cols : tokens;
+  size_t most = 0;
+  for (const int64_t t : {tokens, tokens / kTiles * kTiles, few, few / kTiles * kTiles}) {
+    const size_t bytes = t > 0 ? embed_layout(t, cols).total : 0;
+    if (bytes > most) most = bytes;
+  }
+  return most;
+}
+
 hipError_t launch_embed(const EmbedLaunch& L) {
   EmbedArgs a;
   a.ids = L.ids;

@@ -291,7 +291,7 @@ zs_status zs_embed_forward(const zs_embed_args* args) {
 
 size_t zs_embed_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols) {
   if (embed_sizes(tokens, rows, cols) != ZS_OK) return 0;
-  return zs::embed_layout(tokens > 0 ? tokens : 1, cols).total;
+  return zs::embed_workspace(tokens > 0 ? tokens : 1, cols);
 }
 
 zs_status zs_embed_backward(const zs_embed_grad_args* args) {

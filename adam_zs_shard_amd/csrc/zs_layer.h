@@ -88,6 +88,8 @@ struct EmbedLayout {
 constexpr int64_t kSortAlone = 16384;
 constexpr int kBucketBits = 8, kSortBits = 10;
 EmbedLayout embed_layout(int64_t tokens, int64_t cols);
+// The most that a call of so many tokens (>= 1) or fewer takes.
+size_t embed_workspace(int64_t tokens, int64_t cols);
 
 struct EmbedGradLaunch {
   int64_t tokens, rows, first_row;

@@ -181,12 +181,13 @@ typedef struct {
 } zs_embed_grad_args;
 
 /* Device bytes for zs_embed_backward (the tokens in the order of their rows,
- * and the sums of rows whose tokens are summed in several parts); 0 on sizes
- * that it refuses. */
+ * and the sums of rows whose tokens are summed in several parts), of so many
+ * tokens or fewer and of so many columns: a buffer for the longest batch does
+ * for all.  0 on sizes that it refuses. */
 size_t zs_embed_workspace_bytes(int64_t tokens, int64_t rows, int64_t cols);
 
-/* Errors: as zs_embed_forward, and ZS_ERR_CAPACITY (the workspace is too small
- * or not 256-byte aligned). */
+/* Errors: as zs_embed_forward, and ZS_ERR_CAPACITY (the workspace is smaller
+ * than what this many tokens take, or not 256-byte aligned). */
 zs_status zs_embed_backward(const zs_embed_grad_args* args);
 
 #ifdef __cplusplus

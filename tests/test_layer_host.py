@@ -255,6 +255,24 @@ def test_binding_refuses_tensors_that_it_cannot_name():
             call()
 
 
+# batches around 2^23 elements (where the windows get longer), 16384 tokens (more launches) and
+# multiples of 262144 (where the tiles get longer)
+@pytest.mark.parametrize("cols", [1, 24, 32, 768, 1000, 4096, 1 << 20])
+def test_workspace_of_a_long_batch_does_for_shorter_ones(cols):
+    few, tiles = (1 << 23) // cols, 256 * 1024
+    ends = [1, few // 2, few, 3 * few // 2, 2 * few, 10_000, 16_384, 20_000, tiles, 2 * tiles, 3 * tiles,
+            few // tiles * tiles, 1_000_000, 1 << 28]
+    tokens = sorted({t + d for t in ends for d in (-1, 0, 1) if 1 <= t + d <= 1 << 28})
+    sizes = [a.zs_embed_workspace_bytes(t, 50257, cols) for t in tokens]
+    assert sizes == sorted(sizes)
+    # no smaller than what a call of any of them asks for; the workspace lies on the ids, which is seen later
+    for i, t in enumerate(tokens):
+        for size in {sizes[i], sizes[-1]}:
+            q = a.zs_embed_grad_args(t, 5, cols, 0, a.ZS_I64, z.ZS_BF16, z.ZS_BF16, 0, 1.0, 1 << 50, 1 << 52, cols,
+                                     1 << 40, 1 << 50, size, None)
+            assert a.lib().zs_embed_backward(q) == z.ZS_ERR_ALIAS, (t, size)
+
+
 # ----------------------------------------------------------------- the references
 
 def _inputs(rows, cols, seed):

@@ -17,6 +17,8 @@ constexpr int64_t kMaxBytes = int64_t{1} << 56;
 
 bool dtype_ok(int32_t dt) { return dt == ZS_F16 || dt == ZS_BF16 || dt == ZS_F32; }
 int64_t size_of(int32_t dt) { return dt == ZS_F32 ? 4 : 2; }
+// Whether the fp32 value that the kernels use is finite.
+bool f32_finite(double x) { return std::isfinite(static_cast<float>(x)); }
 
 zs_status from_hip(hipError_t e) {
   return e == hipSuccess ? ZS_OK : static_cast<zs_status>(zs::hip_status(e));
@@ -110,7 +112,7 @@ zs_status workspace_ok(const void* at, size_t bytes, size_t need) {
 zs_status norm_forward(const zs_norm_args* q) {
   if (!q) return ZS_ERR_NULL;
   if (const zs_status st = norm_sizes(q->rows, q->cols, q->kind)) return st;
-  if (!std::isfinite(q->eps) || q->eps < 0.0 || q->reserved != 0) return ZS_ERR_ARG;
+  if (!f32_finite(q->eps) || q->eps < 0.0 || q->reserved != 0) return ZS_ERR_ARG;
   if (!dtype_ok(q->dtype) || !dtype_ok(q->w_dtype)) return ZS_ERR_DTYPE;
   if (q->rows == 0) return ZS_OK;
   const int64_t size = size_of(q->dtype), wsize = size_of(q->w_dtype);
@@ -201,7 +203,7 @@ bool id_dtype_ok(int32_t dt) { return dt == ZS_I32 || dt == ZS_I64; }
 zs_status embed_forward(const zs_embed_args* q) {
   if (!q) return ZS_ERR_NULL;
   if (const zs_status st = embed_sizes(q->tokens, q->rows, q->cols)) return st;
-  if (q->first_row < 0 || !std::isfinite(q->scale) || q->reserved != 0) return ZS_ERR_ARG;
+  if (q->first_row < 0 || !f32_finite(q->scale) || q->reserved != 0) return ZS_ERR_ARG;
   if (q->pos_table && q->pos_rows < 1) return ZS_ERR_ARG;
   if (q->pos_table && q->pos_rows > ZS_EMBED_MAX_ROWS) return ZS_ERR_RANGE;
   if (!dtype_ok(q->dtype) || !dtype_ok(q->table_dtype) || !id_dtype_ok(q->id_dtype)) return ZS_ERR_DTYPE;
@@ -237,7 +239,7 @@ zs_status embed_forward(const zs_embed_args* q) {
 zs_status embed_backward(const zs_embed_grad_args* q) {
   if (!q) return ZS_ERR_NULL;
   if (const zs_status st = embed_sizes(q->tokens, q->rows, q->cols)) return st;
-  if (q->first_row < 0 || !std::isfinite(q->scale) || (q->accumulate != 0 && q->accumulate != 1))
+  if (q->first_row < 0 || !f32_finite(q->scale) || (q->accumulate != 0 && q->accumulate != 1))
     return ZS_ERR_ARG;
   if (!dtype_ok(q->dtype) || !dtype_ok(q->grad_dtype) || !id_dtype_ok(q->id_dtype)) return ZS_ERR_DTYPE;
   if (q->tokens == 0 && q->accumulate) return ZS_OK;

@@ -55,7 +55,7 @@ typedef struct {
   int32_t dtype;           /* of x, residual, total and y */
   int32_t w_dtype;         /* of gamma and beta */
   int32_t reserved;        /* 0 */
-  double eps;              /* finite, >= 0 */
+  double eps;              /* >= 0; used as fp32, finite there */
   const void* x;
   const void* residual;    /* or NULL: t = x, and total is not looked at */
   void* total;             /* written where there is a residual */
@@ -135,7 +135,7 @@ typedef struct {
   int32_t dtype;           /* of y */
   int32_t table_dtype;     /* of table and pos_table */
   int32_t reserved;        /* 0 */
-  double scale;            /* finite */
+  double scale;            /* used as fp32, finite there */
   const void* ids;
   const void* table;       /* rows x cols, contiguous */
   void* y;                 /* tokens rows, written */
@@ -170,7 +170,7 @@ typedef struct {
   int32_t dtype;           /* of dy */
   int32_t grad_dtype;      /* of grad */
   int32_t accumulate;
-  double scale;            /* finite */
+  double scale;            /* used as fp32, finite there */
   const void* ids;
   const void* dy;          /* tokens rows */
   int64_t dy_stride;

@@ -87,6 +87,25 @@ def test_norm_refuses():
         norm(cols=0, check=True)
 
 
+# doubles whose nearest fp32 is infinite; 3.4028235e38 still is the largest finite one
+BEYOND_F32 = [1e39, 3.5e38, 1e300]
+LARGEST_F32 = 3.4028235e38
+
+
+@no_device
+def test_refuses_what_fp32_does_not_hold():
+    for v in BEYOND_F32:
+        assert norm(eps=v) == z.ZS_ERR_ARG
+        for x in (v, -v):
+            assert embed(scale=x) == z.ZS_ERR_ARG
+            assert embed_grad(scale=x) == z.ZS_ERR_ARG
+    # what it holds gets as far as the operands
+    assert norm(eps=LARGEST_F32, x=None) == z.ZS_ERR_NULL
+    for x in (LARGEST_F32, -LARGEST_F32):
+        assert embed(scale=x, ids=None) == z.ZS_ERR_NULL
+        assert embed_grad(scale=x, dy=None) == z.ZS_ERR_NULL
+
+
 @no_device
 def test_norm_refuses_overlap():
     size = (3 * 100 + 100) * 2

@@ -685,6 +685,79 @@ def test_offsets_beyond_32_bits():
     assert float(table[1:rows - 2].abs().max()) == 0.0
 
 
+# ----------------------------------------------------------------- the kernels that large inputs take
+
+def many_tokens(tokens, rows, cols, dt, gdt, accumulate, seed, gap=0):
+    """Whole numbers, so that any order gives the same sums, compared on the device.  Half of the tokens name few
+    rows (whose tokens are summed in parts), a quarter name rows evenly, and the others none."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    row = torch.randint(0, rows, (tokens,), generator=g, device=DEV)
+    kind = torch.rand(tokens, generator=g, device=DEV)
+    row = torch.where(kind < 0.5, row % 40, torch.where(kind < 0.75, row, torch.full_like(row, -1)))
+    dy = torch.randint(-4, 5, (tokens, cols + gap), generator=g, device=DEV, dtype=torch.int8).to(TD[dt])[:, :cols]
+    old = torch.randint(-9, 10, (rows, cols), generator=g, device=DEV, dtype=torch.int8)
+    grad = Buf(1, rows * cols, TD[gdt], 1, 0, old.view(1, -1))
+    nb = a.zs_embed_workspace_bytes(tokens, rows, cols)
+    ws = garbage(nb + 256)
+    a.zs_embed_backward(tokens, row, rows, cols, dy, grad.t[0], ws, nb, accumulate=accumulate)
+    want = old.float() if accumulate else torch.zeros(rows, cols, device=DEV)
+    inside = row >= 0
+    want.index_add_(0, row[inside], dy[inside].float())
+    assert torch.equal(grad.t[0].view(rows, cols), want.to(TD[gdt]))
+    grad.check("grad")
+    assert bool((ws[nb:] == 0xFF).all())
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("gdt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_embed_grad_of_many_tokens(dt, gdt, accumulate):
+    """More than 2^23 elements of dy, in whole packs and in broken ones, sorted in one launch and in several."""
+    for i, (tokens, cols) in enumerate([(8400, 1000), (8200, 1025), (16_500, 515), (33_000, 256)]):
+        many_tokens(tokens, 3001, cols, dt, gdt, accumulate, seed=i, gap=i % 2)
+
+
+@pytest.mark.parametrize("cols", [1000, 1001, 1004, 4096])
+@pytest.mark.parametrize("gdt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+def test_embed_grad_of_more_than_the_cache_keeps(dt, gdt, cols):
+    """More than 64 MiB of dy, added to a gradient: read past the cache."""
+    tokens = (1 << 26) // (cols * (4 if dt == "f32" else 2)) + 1
+    many_tokens(tokens, 700, cols, dt, gdt, True, seed=cols)
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cols", [512, 4096, 16384])
+def test_norm_of_more_than_the_cache_keeps(kind, residual, dt, cols):
+    """More than 192 MiB read and written: read past the cache.  Against the 64-bit reference, on the device."""
+    each = cols * (4 if dt == "f32" else 2) * (4 if residual else 2)
+    rows = (192 << 20) // each + 1
+    g = torch.Generator(device=DEV).manual_seed(cols)
+    x = torch.randn(rows, cols, generator=g, device=DEV) * (0.2 + 2 * torch.rand(rows, 1, generator=g, device=DEV))
+    x[:, :: 97] *= 15
+    x = x.to(TD[dt])
+    r = torch.randn(rows, cols, generator=g, device=DEV).to(TD[dt]) if residual else None
+    total = torch.empty_like(x) if residual else None
+    y, rstd = torch.empty_like(x), torch.empty(rows, device=DEV)
+    mean = torch.empty(rows, device=DEV) if kind == "layer" else None
+    gamma, beta = weights(cols, "f32", 3, (True, True))
+    a.zs_norm_forward(rows, cols, x, y, gamma, beta, kind=kind, eps=EPS, residual=r, total=total, mean=mean, rstd=rstd)
+    t = x
+    if residual:
+        t = (x.float() + r.float()).to(TD[dt])
+        assert torch.equal(total, t)
+    for i in range(0, rows, 4096):
+        at = slice(i, i + 4096)
+        with torch.device(DEV):
+            want = ref.norm(t[at].double(), gamma.double(), beta.double(), kind, float(np.float32(EPS)), TD[dt])
+        for got, name in ((y, "y"), (rstd, "rstd"), (mean, "mean")):
+            if got is not None:
+                value, bound = want[name]
+                assert bool(((got[at].double() - value).abs() <= bound).all()), name
+
+
 class Layer:
     """One batch through the lookup, a norm and their backward passes, all buffers kept."""
 

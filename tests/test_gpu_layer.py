@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import layer_diff
 import layer_ref as ref
 from adam_zs_shard_amd import zsadamw as aw
 from adam_zs_shard_amd import zslayer as a
@@ -445,6 +446,27 @@ def test_norm_grad_against_differences(kind):
         moved = 2 * 4 * ref.U * float((dy.abs().double() * (1 + gamma.abs().max().cpu().double())).sum())
         third = h * h / 6 * 60 * float(dy.double().norm(dim=1).sum()) / cols
         assert abs(got - float(u - v) / (2 * h)) <= float(bu + bv + moved) / (2 * h) + third
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+@pytest.mark.parametrize("rows,cols", [(40, 768), (1200, 768), (30, 1001)])
+def test_norm_grad_against_close_differences(kind, rows, cols):
+    """Row by row, within 2% of the derivative (layer_diff derives by how much); 1200 rows take two launches."""
+    x, dy, gamma, beta = layer_diff.inputs(rows, cols, rows + cols)
+    G, B = gamma.to(DEV), beta.to(DEV)
+
+    def forward(x, gamma, beta, **kw):
+        y = torch.empty(rows, cols, device=DEV)
+        a.zs_norm_forward(rows, cols, x.to(DEV), y, gamma.to(DEV), beta.to(DEV), kind=kind, eps=EPS, **kw)
+        return y.cpu()
+
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    forward(x, G, B, mean=mean, rstd=rstd)
+    dx, dg, db = torch.empty(rows, cols, device=DEV), torch.empty(cols, device=DEV), torch.empty(cols, device=DEV)
+    nb = a.zs_norm_workspace_bytes(rows, cols)
+    a.zs_norm_backward(rows, cols, dy.to(DEV), x.to(DEV), rstd, dx, mean=mean, gamma=G, dgamma=dg, dbeta=db,
+                       kind=kind, workspace=garbage(nb), ws_bytes=nb)
+    layer_diff.check(forward, x, dy, gamma, beta, kind, float(np.float32(EPS)), dx.cpu(), dg.cpu(), db.cpu())
 
 
 # ----------------------------------------------------------------- the table

@@ -10,6 +10,7 @@ import re
 import pytest
 import torch
 
+import layer_diff
 import layer_ref as ref
 from adam_zs_shard_amd import zshard as z
 from adam_zs_shard_amd import zslayer as a
@@ -331,6 +332,40 @@ def test_norm_reference_against_autograd_and_differences(kind):
         up[i], down[i] = args[i] + h * d, args[i] - h * d
         diff = ((forward(*up) - forward(*down)) * dy).sum() / (2 * h)
         assert abs(diff - (got[name][0] * d).sum()) < 1e-7 * (1 + abs(diff)), name
+
+
+def _gradients(x, dy, gamma, kind, eps, leave_out=()):
+    """The formulas in 64 bits, rounded to fp32, less some of their terms."""
+    x, dy, gamma = x.double(), dy.double(), gamma.double()
+    u = x - x.mean(1, keepdim=True) if kind == "layer" else x
+    r = (u.square().mean(1, keepdim=True) + eps).rsqrt()
+    a, h = dy * gamma, u * r
+    dx = a - h * (a * h).mean(1, keepdim=True) * ("c2" not in leave_out)
+    if kind == "layer" and "c1" not in leave_out:
+        dx = dx - a.mean(1, keepdim=True)
+    return [t.float() for t in (dx * r, (dy * h).sum(0), dy.sum(0))]
+
+
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_differences_tell_wrong_gradients(kind):
+    eps = 1e-5
+    x, dy, gamma, beta = layer_diff.inputs(40, 768, 808)
+
+    def forward(x, gamma, beta):
+        return ref.norm(x.double(), gamma.double(), beta.double(), kind, eps, torch.float32)["y"][0].float()
+
+    dx, dg, db = _gradients(x, dy, gamma, kind, eps)
+    layer_diff.check(forward, x, dy, gamma, beta, kind, eps, dx, dg, db)
+    one_row = dx.clone()
+    one_row[17] = 0
+    wrong = [(0 * dx, dg, db), (-dx, dg, db), (1.03 * dx, dg, db), (one_row, dg, db),
+             (_gradients(x, dy, gamma, kind, eps, ["c2"])[0], dg, db), (dx, 1.03 * dg, db), (dx, -dg, db),
+             (dx, dg, 0 * db), (dx, dg, 1.03 * db), (dx, db, dg)]
+    if kind == "layer":
+        wrong.append((_gradients(x, dy, gamma, kind, eps, ["c1"])[0], dg, db))
+    for got in wrong:
+        with pytest.raises(AssertionError):
+            layer_diff.check(forward, x, dy, gamma, beta, kind, eps, *got)
 
 
 def test_embed_reference_against_autograd():

@@ -5,12 +5,12 @@
 // are few: each row's address waits for the token's id.
 //
 // The gradient's row r is the sum of the rows of dy whose tokens name r, in the
-// tokens' order and without atomics, so that it has the same bits every time.  The
-// tokens are sorted by row, stably (one launch, or two per digit of the row for many
-// tokens); the sorted list is cut into windows, and a wave sums the rows of dy of one
-// window and 1 KiB of columns.  A table row with more tokens than a window has
-// places is summed in parts, which go to the workspace, and a last kernel adds them
-// in their order.  With accumulate = 0 the table is cleared by the launch that
+// tokens' order and without atomics on floating-point numbers, so that it has the same
+// bits every time.  The tokens are sorted by row, stably (one launch, or two per digit
+// of the row for many tokens); the sorted list is cut into windows, and a wave sums
+// the rows of dy of one window and 1 KiB of columns.  A table row with more tokens
+// than a window has places is summed in parts, which go to the workspace, and a last
+// kernel adds them in their order.  With accumulate = 0 the table is cleared by the launch that
 // sorts, beside it; so the rows that tokens name are written twice, 45 MB of the 1.1
 // GB that 16384 tokens of a 128256 x 4096 table move, for 20 us of sorting that
 // nothing waits for.
@@ -199,7 +199,9 @@ constexpr int kBuckets = 64;
 constexpr int kFew = 512;
 // Where all workgroups go through all tokens, their time grows with these: 2048, 4096,
 // 8192 and 16384 tokens 6, 8.5, 11.5 and 19 us; 131072 97, where the passes below
-// take 25.
+// take 25.  All of the gradient with this sort and with the passes, us: 2048 x 64,
+// added to 50257 rows, 15.5 / 23.6, 8192 20.7 / 28.8, 12288 26.3 / 32.3, 16384 29.2 /
+// 29.4, 16384 x 768 35.5 / 31.4.
 constexpr int kIdSteps = 8;  // steps of 64 tokens whose ids a wave loads together
 
 // A wave's run of the tokens; the rows of its first kIdSteps steps stay in registers.
@@ -521,10 +523,11 @@ __device__ __forceinline__ void for_units(int64_t units, F&& f) {
 }
 
 // A window is W places of the sorted list.  The wave of a window and slab of
-// columns sums every table row whose tokens begin in the window, as far as they go,
-// if they are at most W.  The tokens of a row that has more (a long row) are
-// summed by each window that they meet: where they begin, to the window's second row
-// of sums, elsewhere to its first; sum_join_kernel adds these.
+// columns (1 KiB of dy's; of narrower rows some lanes have none) sums every table row
+// whose tokens begin in the window, as far as they go, if they are at most W.  The
+// tokens of a row that has more (a long row) are summed by each window that they
+// meet: where they begin, to the window's second row of sums, elsewhere to its first;
+// sum_join_kernel adds these.
 //
 // What is where shows in masks of the 3 * W places from W before the
 // window's first: bit l of `on` says that place l holds the row of place l - 1.
@@ -802,9 +805,12 @@ constexpr int64_t kClearLong = int64_t{256} << 20;
 
 // Up to so many bytes, dy may still be in the 256 MB cache where its rows are added to
 // a gradient, and is read through it (us through it and past it: 16384 x 1024 37.3 /
-// 39.9, 4096 x 4096 28.1 / 31.0, 32768 x 768 42.3 / 43.8, 131072 x 1024 122 / 106);
-// where the gradient was cleared before, that has filled the cache (16384 x 1024 52.0 /
-// 43.3, 32768 x 768 53.2 / 49.1).
+// 39.9, 4096 x 4096 28.1 / 31.0, 32768 x 768 42.3 / 43.8, 131072 x 1024 122 / 106).
+// Into a gradient that was cleared before it is read past it: a large one has filled
+// the cache (16384 x 1024 52.0 / 43.3, 32768 x 768 53.2 / 49.1), and small ones gain
+// more by it than they lose (a position table's: 8192 x 768 into 1024 rows 15.2 / 13.4,
+// 32768 x 768 into 1024 rows 43.9 / 45.7, 16384 x 4096 into 8192 rows 66.9 / 58.3;
+// 8192 x 768 into 2000 rows 24.6 / 24.4).
 constexpr int64_t kSumCached = int64_t{64} << 20;
 static_assert(kWindowElems * 4 <= kSumCached, "few tokens' rows are read through it");
 

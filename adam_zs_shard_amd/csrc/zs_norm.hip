@@ -131,7 +131,10 @@ constexpr int kNormHeld = 16384;
 // Where a call reads and writes more than this, its rows do not stay in the 256 MB
 // cache from one kernel of a model to the next, and it reads past that (16384 x 4096
 // with a residual 85.9 us, 89.8 read through it); smaller ones may have been left
-// there by the kernel before (32768 x 1024 bf16 22.4 us, read past it 27.4).
+// there by the kernel before (32768 x 1024 bf16 22.4 us, read past it 27.4).  Rows of
+// broken packs are read through it at any size, since it makes no difference there:
+// 40,000 x 1001 with a residual 63.8 us, past it 62.3, 16384 x 4099 154 and 154, 60,000
+// x 1001 without one 50.4 and 50.8.
 constexpr int64_t kNormCached = int64_t{192} << 20;
 
 constexpr int norm_group(int team) { return team <= kWave ? 4 * kWave : team; }

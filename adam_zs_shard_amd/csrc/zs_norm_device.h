@@ -51,6 +51,10 @@ __device__ __forceinline__ void team_sums(float (&x)[N], float (*part)[N][16], i
 // Teams of 16 and 32 lanes share a wave: a wave to each row is 262,144 x 128 bf16 rms
 // forward 52.1 us for 22.3 and backward 75.2 for 37.2, 40,000 x 256 13.6 for 8.5 and
 // 22.7 for 19.2.
+// Teams double, so that rows between two sizes leave lanes without elements: layer
+// norm, bf16, TB/s forward and backward, 8192 x 8192 5.7 and 4.6, 8192 x 5120 4.9 and
+// 3.7, 8192 x 6144 4.8 and 3.9, 4096 x 12288 4.0 and 3.4, 16384 x 1280 4.5 and 3.4,
+// 16384 x 1600 5.1 and 4.1, 16384 x 2560 5.2 and 3.8.
 template <int E, class F>
 void with_shape(int dt, int cols, F&& f) {
   with_gdt(dt, [&](auto d) {

@@ -10,6 +10,12 @@
 // CU, without the next row in flight: 16384 x 4096 bf16 with a gradient that passes
 // by 93.5 us in all, three 102 to 107, four 107.5, one with the next row 116, two
 // with it 94.5; 8192 x 768 16.0, 15.0, 18.8, 19.7 and 16.6.
+//
+// dy, x and dres are read past the cache whatever their size (us so and through it,
+// bf16: 16384 x 4096 with a gradient that passes by 93.4 / 100.2, 32768 x 4096 151 /
+// 153, 65536 x 1024 75.5 / 77.7, 32768 x 1024 42.4 / 43.2).  Inputs of less than 100
+// MB, which the kernel before may have left there, pay for it: 8192 x 768 15.0 / 13.5,
+// 16384 x 768 22.2 / 20.0, 4096 x 4096 30.9 / 27.5.
 
 #include "zs_norm_device.h"
 
@@ -261,7 +267,8 @@ __global__ __launch_bounds__(WG) void norm_grad_kernel(NormGradArgs a) {
 }
 
 // The rows of sums, added in a fixed order: 16 places and 64 parts of the rows
-// per workgroup, eight loads of a lane in flight.
+// per workgroup, eight loads of a lane in flight.  16 places are half of a line of the
+// cache, so two workgroups read each (16384 x 4096: 16.1 MiB of 8).
 constexpr int kJoinCols = 16, kJoinParts = 64, kJoinLoads = kNormParts / kJoinParts;
 
 struct NormJoinArgs {

@@ -16,8 +16,8 @@
  * nearest even.  The fp32 operations are those written below, each rounded
  * once (correctly rounded division and root); only a product that goes straight
  * into a sum over a row or over rows is not rounded before it is added.  Such
- * sums are in an order that is fixed by the call's sizes, whether it is in
- * place, and the device: the same bits every time.  Infinities and NaN
+ * sums are in an order that is fixed by the call's sizes and types, whether it
+ * is in place, and the device: the same bits every time.  Infinities and NaN
  * propagate by IEEE rules, within their row and into the gradients' sums.
  *
  * Rows of activations are row-major with a stride in elements, at least cols;
@@ -109,8 +109,9 @@ typedef struct {
   void* stream;
 } zs_norm_grad_args;
 
-/* Device bytes for the sums of zs_norm_backward's gradients; 0 on sizes that
- * it refuses. */
+/* Device bytes for the sums of zs_norm_backward's gradients: 4 KiB for each of
+ * cols rounded up to a power of two, 512 at least, whatever the rows; 0 on sizes
+ * that it refuses. */
 size_t zs_norm_workspace_bytes(int64_t rows, int64_t cols);
 
 /* Bytes per element: 3 (4 with dres) elements of dtype.  In place: dx may be

@@ -20,8 +20,9 @@ TD = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 def column_adds(rows):
     """The same for a sum over rows.  A lane adds those of its own turns: a 128th of
     the rows at most where a launch has all 256 CUs' workgroups, and of 1024 rows at
-    most where few are read by columns, a 64th, 16.  Then come at most 16 teams or
-    waves, 512 parts by 64 in 8 turns and in 6 steps."""
+    most where few are read by columns, a 64th, 16.  Then come at most 16 waves, or
+    32 teams (of 16 lanes), and 512 parts by 64 in 8 turns and in 6 steps: 46 of the
+    64 here."""
     return min(rows, rows // 128 + 1) + 16 + 16 + 32
 
 
